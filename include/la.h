@@ -60,7 +60,9 @@ typedef uint16_t la_bf16; /* bfloat16 bits */
 typedef void *la_stream;  /* cudaStream_t */
 
 /* Device status word bits, set by kernels, read by la_device_status(). */
-#define LA_DEV_TIMEOUT 0x1u /* a bounded mbarrier / flag wait gave up */
+#define LA_DEV_TIMEOUT 0x1u   /* a bounded mbarrier / flag wait gave up */
+#define LA_DEV_BAD_INDEX 0x2u /* a cache call met a length or a page number out of range */
+#define LA_DEV_NONFINITE 0x4u /* la_cache_write met an infinity or a NaN */
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *la_status_string(la_status s);
@@ -304,6 +306,100 @@ la_status la_decode_step(float *S, const la_bf16 *q, const la_bf16 *k, const la_
  * N = steps); S as la_decode_step.  Errors as la_decode_step. */
 la_status la_decode_steps(float *S, const la_bf16 *q, const la_bf16 *k, const la_bf16 *v,
                           la_bf16 *o, int B, int Hq, int Hkv, int d, int steps, la_stream stream);
+
+/* ------------------------------------------------------------------------
+ * An 8-bit key/value cache, and softmax attention over it, for the softmax
+ * layers of a hybrid stack (one after every seven lightning layers in the
+ * pages' model): written, read back and attended to on the device.
+ *
+ * Layout.  Keys and values live in pages of `page` tokens.  A page holds, for
+ * each kv head, page x d codes of 8 bits (e4m3: 4 exponent and 3 mantissa bits,
+ * largest number 448) and one fp32 scale, a power of two; the cache stands for
+ * code * scale.  Keys and values have codes and scales of their own:
+ *     k_codes, v_codes  [num_pages, Hkv, page, d]    8 bits each
+ *     k_scale, v_scale  [num_pages, Hkv]             fp32
+ * Sequence b's token t is row t % page of page table[b][t / page]; table is
+ * [B, max_pages] int32.  Only the entries that a call's tokens need are read, so
+ * the rest may hold anything.  Pages may be shared by sequences that only read
+ * them (a common prompt); a page that a call writes must belong to one sequence.
+ *
+ * Lengths (start, count, kv_len, q_len) are int32 [B] device arrays, so a
+ * captured graph follows them as they change; a null count or q_len stands for N
+ * everywhere.  The kernels check lengths and page numbers against max_pages,
+ * N and num_pages: a sequence with a length out of range is left out (nothing of
+ * it is written), a page number out of range is not followed (its tokens are
+ * not written, or taken as zeros), and LA_DEV_BAD_INDEX is set.
+ *
+ * page in {16, 32, 64, 128}, d in {64, 128}; num_pages * Hkv * page < 2^31.
+ * ---------------------------------------------------------------------- */
+typedef enum { LA_BF16 = 0, LA_FP16 = 1, LA_F32 = 2 } la_dtype;
+
+typedef struct {
+  uint8_t *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  int64_t num_pages;
+  int32_t Hkv, page, d;
+} la_cache;
+
+/* Stores tokens start[b] .. start[b] + count[b] - 1 of every sequence from
+ * k, v [B,Hkv,N,d] (bf16, fp16 or fp32; row i is token start[b] + i).  For each
+ * page and head that they touch:
+ *     scale = 2^e with the least e >= -126 for which max |x| <= 448 * 2^e over
+ *             the new tokens; not less than the page's scale if it already
+ *             holds tokens of the sequence (start[b] inside the page)
+ *     code  = x / scale rounded to nearest even
+ * When the scale grows, the page's older codes are rounded to the new one (exact
+ * but for those that fall below the least normal code).  Rows behind the last
+ * token are left as they were, and so are rows i >= count[b] of k and v unread.
+ * The cache holds finite numbers only: an infinity is stored as the largest code
+ * of its sign, a NaN as zero, neither counts for the scale, and
+ * LA_DEV_NONFINITE is set.
+ * Errors: LA_ERR_INVALID_ARG (null, misaligned or overlapping pointers, sizes
+ * <= 0, an unknown dtype), LA_ERR_UNSUPPORTED (page or d). */
+la_status la_cache_write(const void *k, const void *v, la_dtype dtype, const la_cache *cache,
+                         const int32_t *table, const int32_t *start, const int32_t *count, int B,
+                         int64_t N, int max_pages, la_stream stream);
+
+/* Reads tokens start[b] .. start[b] + count[b] - 1 back into k, v [B,Hkv,N,d]
+ * of the given type: code * scale rounded once to it (exact in fp32, and in bf16
+ * where the exponent allows).  Rows i >= count[b] are left as they were.
+ * Errors as la_cache_write. */
+la_status la_cache_read(const la_cache *cache, const int32_t *table, const int32_t *start,
+                        const int32_t *count, void *k, void *v, la_dtype dtype, int B, int64_t N,
+                        int max_pages, la_stream stream);
+
+/* Causal softmax attention over the cache.  Sequence b has kv_len[b] tokens in
+ * it, and its q_len[b] queries (rows i < q_len[b] of q [B,Hq,N,d]) are the last
+ * of them: query i is token kv_len[b] - q_len[b] + i and sees the tokens up to
+ * itself.  With p_ij = exp(scale * q_i . k_j) over those tokens j,
+ *     o_i = sum_j p_ij v_j / sum_j p_ij,      lse_i = ln sum_j p_ij
+ * for every query head of the kv head's group.  One call serves a decode step
+ * (N = 1), a few drafted tokens, a whole prompt, or a later piece of one; the
+ * tokens themselves are stored by la_cache_write first.  A query that sees no
+ * token (q_len[b] > kv_len[b]) gives o = 0, lse = -infinity.  Rows i >= q_len[b]
+ * of o and lse are left as they were.
+ *   q, o      bf16 or fp16 [B,Hq,N,d], o not overlapping q or the cache
+ *   lse       fp32 [B,Hq,N], or null
+ *   scale     finite; usually 1/sqrt(d)
+ * Scores, the softmax's sums and the products are held in fp32.
+ * Splits long sequences over the SMs and joins the parts; the parts' workspace
+ * comes from the stream-ordered pool (la_cache_attend) or from the caller
+ * (la_cache_attend_ws: 256-byte aligned, at least
+ * la_cache_attend_workspace_bytes(), not in use by anything else until the
+ * call's work has finished: captured graphs that may run at the same time need
+ * one each).  The same inputs give the same bits.
+ * Errors as la_cache_write; LA_ERR_UNSUPPORTED also for Hq / Hkv > 32, B > 4096
+ * and fp32; LA_ERR_WORKSPACE. */
+size_t la_cache_attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d);
+la_status la_cache_attend(const void *q, la_dtype dtype, const la_cache *cache,
+                          const int32_t *table, const int32_t *kv_len, const int32_t *q_len,
+                          void *o, float *lse, int B, int Hq, int64_t N, int max_pages, float scale,
+                          la_stream stream);
+la_status la_cache_attend_ws(const void *q, la_dtype dtype, const la_cache *cache,
+                             const int32_t *table, const int32_t *kv_len, const int32_t *q_len,
+                             void *o, float *lse, int B, int Hq, int64_t N, int max_pages,
+                             float scale, void *workspace, size_t workspace_bytes,
+                             la_stream stream);
 
 /* ------------------------------------------------------------------------
  * Failure detection.

@@ -8,8 +8,10 @@ The shared library is loaded on first use and a missing build is an error.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -27,7 +29,9 @@ EXPORTS = ("la_status_string", "la_version", "la_forward", "la_forward_state",
            "la_forward_host", "la_prefill_fused_workspace_bytes", "la_prefill_fused",
            "la_prefill_plan", "la_backward", "la_segment_state", "la_state_prefix",
            "la_prefill_span_states", "la_prefill_scan", "la_prefill_main", "la_forward_f32",
-           "la_decode_step", "la_decode_steps", "la_device_status", "la_selftest_wait",
+           "la_decode_step", "la_decode_steps", "la_cache_write", "la_cache_read",
+           "la_cache_attend_workspace_bytes", "la_cache_attend", "la_cache_attend_ws",
+           "la_device_status", "la_selftest_wait",
            "la_shutdown")
 
 
@@ -43,13 +47,32 @@ class la_plan(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_int64)]
 
 
+class _la_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("Hkv", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class la_cache(NamedTuple):
+    """An 8-bit key/value cache in pages: codes [num_pages,Hkv,page,d] float8_e4m3fn
+    and scales [num_pages,Hkv] float32 (CUDA) of the keys and of the values."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
 def library_path() -> str:
     return os.environ.get("LA_LIBRARY", os.path.join(_HERE, _LIBNAME))
 
 
 def _declare(lib):
     P, I, L, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-    PP = ctypes.POINTER(la_plan)
+    PP, PC, F = ctypes.POINTER(la_plan), ctypes.POINTER(_la_cache), ctypes.c_float
     sig = {
         "la_status_string": ([I], ctypes.c_char_p),
         "la_version": ([], I),
@@ -71,6 +94,11 @@ def _declare(lib):
         "la_state_prefix": ([P, P, P, I, I, I, I, I, P], I),
         "la_decode_step": ([P, P, P, P, P, I, I, I, I, P], I),
         "la_decode_steps": ([P, P, P, P, P, I, I, I, I, I, P], I),
+        "la_cache_write": ([P, P, I, PC, P, P, P, I, L, I, P], I),
+        "la_cache_read": ([PC, P, P, P, P, P, I, I, L, I, P], I),
+        "la_cache_attend_workspace_bytes": ([I, I, I, L, I], S),
+        "la_cache_attend": ([P, I, PC, P, P, P, P, P, I, I, L, I, F, P], I),
+        "la_cache_attend_ws": ([P, I, PC, P, P, P, P, P, I, I, L, I, F, P, S, P], I),
         "la_device_status": ([ctypes.POINTER(ctypes.c_uint), I], I),
         "la_selftest_wait": ([L, P], I),
         "la_shutdown": ([], None),
@@ -340,6 +368,114 @@ def la_decode_steps(S, q, k, v, o=None, stream=None):
         o = torch.empty_like(q)
     _check("la_decode_steps", load_library().la_decode_steps(
         _ptr(S), _ptr(q), _ptr(k), _ptr(v), _ptr(o), B, Hq, k.shape[1], d, steps, _stream(stream)))
+    return o
+
+
+def _cache(fn, cache, table, lengths, tensors):
+    """The C view of a cache after checks of it, of the page table, of the int32
+    [B] arrays `lengths` (None allowed) and of the devices of all of them."""
+    kc = cache.k_codes
+    for name in ("k_codes", "v_codes"):
+        _need(fn, name, getattr(cache, name), torch.float8_e4m3fn)
+    for name in ("k_scale", "v_scale"):
+        _need(fn, name, getattr(cache, name), torch.float32)
+    if (kc.dim() != 4 or cache.v_codes.shape != kc.shape or cache.k_scale.shape != kc.shape[:2]
+            or cache.v_scale.shape != kc.shape[:2]):
+        raise ValueError(f"{fn}: expected codes [num_pages,Hkv,page,d] and scales [num_pages,Hkv]; "
+                         f"got {[tuple(t.shape) for t in cache]}")
+    _need(fn, "table", table, torch.int32)
+    if table.dim() != 2:
+        raise ValueError(f"{fn}: table must be [B,max_pages], not {tuple(table.shape)}")
+    for name, t in lengths.items():
+        _need(fn, name, t, torch.int32)
+        if t is not None and tuple(t.shape) != (table.shape[0],):
+            raise ValueError(f"{fn}: {name} must be [{table.shape[0]}], not {tuple(t.shape)}")
+    dev = kc.device
+    for t in (*cache, table, *lengths.values(), *tensors):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{fn}: tensors on {dev} and on {t.device}")
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: tensors on {dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    P, Hkv, page, d = kc.shape
+    return _la_cache(kc.data_ptr(), cache.v_codes.data_ptr(), cache.k_scale.data_ptr(),
+                     cache.v_scale.data_ptr(), P, Hkv, page, d)
+
+
+def _cache_kv(fn, cache, table, k, v):
+    """k, v [B,Hkv,N,d] of one of the three types that fit the cache and the table -> (dtype, N)."""
+    _need(fn, "k", k)
+    _need(fn, "v", v)
+    P, Hkv, page, d = cache.k_codes.shape
+    if (k.dim() != 4 or k.shape != v.shape or tuple(k.shape[:2]) != (table.shape[0], Hkv)
+            or k.shape[3] != d):
+        raise ValueError(f"{fn}: expected k, v [{table.shape[0]},{Hkv},N,{d}]; got k "
+                         f"{tuple(k.shape)}, v {tuple(v.shape)}")
+    if k.dtype != v.dtype or k.dtype not in DTYPES:
+        raise ValueError(f"{fn}: k and v must be of one type, bfloat16, float16 or float32, not "
+                         f"{k.dtype} and {v.dtype}")
+    return DTYPES[k.dtype], k.shape[2]
+
+
+def la_cache_write(k, v, cache: la_cache, table, start, count=None, stream=None):
+    """Store tokens start[b] + i, i < count[b] (or N), from k, v [B,Hkv,N,d] (bf16, fp16
+    or fp32, CUDA) in the pages table [B,max_pages]; start, count int32 [B]."""
+    c = _cache("la_cache_write", cache, table, {"start": start, "count": count}, (k, v))
+    dtype, N = _cache_kv("la_cache_write", cache, table, k, v)
+    _check("la_cache_write", load_library().la_cache_write(
+        _ptr(k), _ptr(v), dtype, ctypes.byref(c), _ptr(table), _ptr(start), _ptr(count),
+        table.shape[0], N, table.shape[1], _stream(stream)))
+
+
+def la_cache_read(cache: la_cache, table, start, k, v, count=None, stream=None):
+    """Tokens start[b] + i, i < count[b] (or N), into k, v [B,Hkv,N,d] (bf16, fp16 or
+    fp32, CUDA), which are returned."""
+    c = _cache("la_cache_read", cache, table, {"start": start, "count": count}, (k, v))
+    dtype, N = _cache_kv("la_cache_read", cache, table, k, v)
+    _check("la_cache_read", load_library().la_cache_read(
+        ctypes.byref(c), _ptr(table), _ptr(start), _ptr(count), _ptr(k), _ptr(v), dtype,
+        table.shape[0], N, table.shape[1], _stream(stream)))
+    return k, v
+
+
+def la_cache_attend_workspace_bytes(B, Hq, Hkv, N, d) -> int:
+    return int(load_library().la_cache_attend_workspace_bytes(B, Hq, Hkv, N, d))
+
+
+def la_cache_attend(q, cache: la_cache, table, kv_len, q_len=None, o=None, lse=None,
+                    scale: float | None = None, workspace=None, stream=None):
+    """Causal softmax attention of the last q_len[b] (or N) of kv_len[b] cached tokens:
+    q [B,Hq,N,d] bf16 or fp16 -> o; lse [B,Hq,N] fp32, if given, is written; scale
+    defaults to 1/sqrt(d).  With a workspace (CUDA, contiguous) the call is
+    la_cache_attend_ws."""
+    fn = "la_cache_attend" if workspace is None else "la_cache_attend_ws"
+    c = _cache(fn, cache, table, {"kv_len": kv_len, "q_len": q_len}, (q, o, lse, workspace))
+    _need(fn, "q", q)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{fn}: q must be bfloat16 or float16, not {q.dtype}")
+    _need(fn, "o", o, q.dtype)
+    _need(fn, "lse", lse, torch.float32)
+    _need(fn, "workspace", workspace)
+    if (q.dim() != 4 or q.shape[0] != table.shape[0] or q.shape[3] != c.d
+            or (o is not None and o.shape != q.shape)):
+        raise ValueError(f"{fn}: expected q, o [{table.shape[0]},Hq,N,{c.d}]; got q "
+                         f"{tuple(q.shape)}" + ("" if o is None else f", o {tuple(o.shape)}"))
+    if lse is not None and lse.shape != q.shape[:3]:
+        raise ValueError(f"{fn}: lse must be {list(q.shape[:3])}, not {tuple(lse.shape)}")
+    if kv_len is None:
+        raise ValueError(f"{fn}: kv_len is required")
+    B, Hq, N, d = q.shape
+    if o is None:
+        o = torch.empty_like(q)
+    args = (_ptr(q), DTYPES[q.dtype], ctypes.byref(c), _ptr(table), _ptr(kv_len), _ptr(q_len),
+            _ptr(o), _ptr(lse), B, Hq, N, table.shape[1],
+            1.0 / math.sqrt(d) if scale is None else scale)
+    if workspace is None:
+        _check(fn, load_library().la_cache_attend(*args, _stream(stream)))
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        _check(fn, load_library().la_cache_attend_ws(*args, _ptr(workspace), nbytes,
+                                                     _stream(stream)))
     return o
 
 

@@ -204,6 +204,11 @@ unsigned* device_status_ptr() {
   return device_info(&st, nullptr) ? st : nullptr;
 }
 
+int device_sms() {
+  int n = 0;
+  return device_info(nullptr, &n) ? n : 0;
+}
+
 bool make_tmap_bf16(CUtensorMap* map, const void* base, int64_t rows_per_head, int64_t heads,
                     int box_rows) {
   {

@@ -1,0 +1,143 @@
+// la_cache.cuh -- what the kernels of the 8-bit key/value cache share: the view
+// of a cache that a launch gets, e4m3 conversions, the sequence lengths.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "la_internal.h"
+
+namespace la {
+
+constexpr unsigned kDevBadIndex = 0x2u;   // LA_DEV_BAD_INDEX
+constexpr unsigned kDevNonfinite = 0x4u;  // LA_DEV_NONFINITE
+
+inline int page_log2(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+// ---------------------------------------------------------------- types
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Eight consecutive values of type T <-> fp32; p is aligned to their size (16
+// bytes, or two loads of 16 for fp32).
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<T>(r[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  uint4 w;
+  w.x = pack2<T>(x[0], x[1]);
+  w.y = pack2<T>(x[2], x[3]);
+  w.z = pack2<T>(x[4], x[5]);
+  w.w = pack2<T>(x[6], x[7]);
+  __stcs(reinterpret_cast<uint4*>(p), w);
+}
+template <>
+__device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+}
+
+// ---------------------------------------------------------------- e4m3
+// Two codes (low byte first) as f16x2, exactly: f16 has e4m3's numbers.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
+      : "=r"(r)
+      : "r"(codes));
+  return r;
+}
+
+// Two fp32 numbers as codes, rounded to nearest even (|x| <= 448 here).
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Exponent of the scale for values of magnitude up to amax (finite, >= 0): the
+// least e >= -126 with amax <= 448 * 2^e = 1.75 * 2^(e + 8).
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, -126);
+}
+
+__device__ __forceinline__ float pow2i(int e) {  // 2^e, -126 <= e <= 127
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// ---------------------------------------------------------------- lengths
+// Tokens [first, first + n) of a sequence: false (and the status bit) when they
+// do not lie in [0, limit); n = 0 is always well.
+__device__ __forceinline__ bool token_range_ok(int64_t first, int64_t n, int64_t nmax,
+                                               int64_t limit, unsigned* status) {
+  if (n == 0) return true;
+  const bool ok = n > 0 && n <= nmax && first >= 0 && first + n <= limit;
+  if (!ok) atomicOr(status, kDevBadIndex);
+  return ok;
+}
+
+// One attention call as its kernels get it.
+struct AttendParams {
+  const void* q;           // [B, Hq, N, d]
+  const uint8_t* codes[2];  // k, v [num_pages, Hkv, page, d]
+  const float* kvscale[2];  // [num_pages, Hkv]
+  const int* table;        // [B, max_pages]
+  const int* kv_len;       // [B]
+  const int* q_len;        // [B] or null (N everywhere)
+  void* o;
+  float* lse;              // [B, Hq, N] or null
+  unsigned* status;
+  int64_t N, num_pages;
+  int B, Hq, Hkv, G, max_pages, page_log2;
+  float scale;
+};
+
+// Whether a sequence's lengths lie in range; if not the sequence is left out.
+__device__ __forceinline__ bool attend_lengths_ok(int64_t kv, int64_t nq, const AttendParams& p) {
+  const bool ok = kv >= 0 && kv <= ((int64_t)p.max_pages << p.page_log2) && nq >= 0 && nq <= p.N;
+  if (!ok) atomicOr(p.status, kDevBadIndex);
+  return ok;
+}
+
+}  // namespace la

@@ -30,6 +30,8 @@ struct PrefillMaps {
 
 // Device address of the status word on the current device (nullptr on failure).
 unsigned* device_status_ptr();
+// SMs of the current device (0 on failure).
+int device_sms();
 // Raises the release threshold of the current device's default memory pool
 // once, so stream-ordered workspaces stay mapped between calls instead of
 // being returned at every synchronisation (la_shutdown trims the pool).
@@ -130,6 +132,22 @@ cudaError_t launch_bwd_walk(const la_bf16* q, const la_bf16* k, const la_bf16* v
                             const la_bf16* dO, la_bf16* dk, la_bf16* dv, const float* ws,
                             float* s_out, unsigned* status, int B, int Hq, int Hkv, int64_t N,
                             int nspan, int num_ctas, cudaStream_t stream, bool dependent);
+// The 8-bit key/value cache (la_cache_* entry points; arguments already checked).
+constexpr int kAttendMaxGroup = 32;    // query heads per kv head
+constexpr int kAttendMaxBatch = 4096;  // sequences of one call
+cudaError_t launch_cache_write(const void* k, const void* v, la_dtype dtype, const la_cache& c,
+                               const int32_t* table, const int32_t* start, const int32_t* count,
+                               int B, int64_t N, int max_pages, unsigned* status,
+                               cudaStream_t stream);
+cudaError_t launch_cache_read(const la_cache& c, const int32_t* table, const int32_t* start,
+                              const int32_t* count, void* k, void* v, la_dtype dtype, int B,
+                              int64_t N, int max_pages, unsigned* status, cudaStream_t stream);
+size_t attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d, int sms);
+cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype,
+                                const int32_t* table, const int32_t* kv_len, const int32_t* q_len,
+                                void* o, float* lse, int B, int Hq, int64_t N, int max_pages,
+                                float scale, void* workspace, unsigned* status, int sms,
+                                cudaStream_t stream);
 cudaError_t launch_selftest_wait(unsigned* status, int64_t timeout_ns, cudaStream_t stream);
 
 }  // namespace la
