@@ -14,6 +14,13 @@ namespace la {
 constexpr unsigned kDevBadIndex = 0x2u;   // LA_DEV_BAD_INDEX
 constexpr unsigned kDevNonfinite = 0x4u;  // LA_DEV_NONFINITE
 
+struct AttendParams;
+struct JoinGeometry;
+cudaError_t launch_cache_token(const AttendParams& p, const la_cache& c, la_dtype dtype, int rows,
+                               int ctas, cudaStream_t stream);
+cudaError_t launch_cache_join(const AttendParams& p, const JoinGeometry& g, la_dtype dtype, int d,
+                              int ctas, cudaStream_t stream);
+
 inline int page_log2(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
 // ---------------------------------------------------------------- types
@@ -119,18 +126,20 @@ __device__ __forceinline__ bool token_range_ok(int64_t first, int64_t n, int64_t
 
 // One attention call as its kernels get it.
 struct AttendParams {
-  const void* q;           // [B, Hq, N, d]
+  const void* q;            // [B, Hq, N, d]
   const uint8_t* codes[2];  // k, v [num_pages, Hkv, page, d]
   const float* kvscale[2];  // [num_pages, Hkv]
-  const int* table;        // [B, max_pages]
-  const int* kv_len;       // [B]
-  const int* q_len;        // [B] or null (N everywhere)
+  const int* table;         // [B, max_pages]
+  const int* kv_len;        // [B]
+  const int* q_len;         // [B] or null (N everywhere)
   void* o;
-  float* lse;              // [B, Hq, N] or null
+  float* lse;               // [B, Hq, N] or null
   unsigned* status;
   int64_t N, num_pages;
   int B, Hq, Hkv, G, max_pages, page_log2;
   float scale;
+  float* parts;             // workspace: [ctas][2] parts of rows x (d + kPartStats) floats
+  int4* tails;              // workspace: [ctas], see below
 };
 
 // Whether a sequence's lengths lie in range; if not the sequence is left out.
@@ -138,6 +147,60 @@ __device__ __forceinline__ bool attend_lengths_ok(int64_t kv, int64_t nq, const 
   const bool ok = kv >= 0 && kv <= ((int64_t)p.max_pages << p.page_log2) && nq >= 0 && nq <= p.N;
   if (!ok) atomicOr(p.status, kDevBadIndex);
   return ok;
+}
+
+// The work of an attention call is a line of equal key tiles: unit after unit (a
+// unit is the query rows that one block works on together: their sequence and
+// kv head, and for prompts a range of tokens), each with the tiles its rows see,
+// at least one.  The line is cut into equal shares, one for each block, so every
+// block has the same work whatever the lengths.  A unit that a cut goes through
+// is computed in parts: the block where it begins writes its part to slot 1 of
+// its two and says in `tails` how many blocks hold the rest; each of those
+// writes slot 0.  A second kernel joins the parts.
+//   part: rows x d fp32 sums (relative to the row's maximum m and to the largest
+//   scale v of the values), then for each row {m, l, v, 0}, m in log2 units
+constexpr int kPartStats = 4;
+// tails[block] = {blocks that hold the rest (0: nothing to join), b, kv head, query tile}
+
+// A unit's rows: `rows` in `blocks` tiles of tile_rows, the first
+// tile_tokens * G of a tile in use: row r of a tile is head r % G of token r / G.
+struct JoinGeometry {
+  int rows, blocks, tile_rows, tile_tokens;
+  float shift;  // weights are 2^shift at the maximum
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kTokenShift = 15.f;  // weights of the token kernel are 2^15 at the maximum
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Sum over the block's threads below this one, and over all (kThreads a multiple
+// of 32, scratch for kThreads / 32 numbers).
+template <int kThreads>
+__device__ __forceinline__ int64_t block_exclusive_sum(int64_t x, int64_t* scratch,
+                                                       int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t in = x;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, in, m);
+    if (lane >= m) in += y;
+  }
+  if (lane == 31) scratch[warp] = in;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  return before + in - x;
 }
 
 }  // namespace la

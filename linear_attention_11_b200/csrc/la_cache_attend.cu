@@ -75,14 +75,46 @@ cudaError_t attend_typed(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+// Calls of at most 32 query rows for each kv head go to the token kernel.
+constexpr int kTokenRows = 32;
+
+struct Shape {
+  bool token;
+  int ctas, rows;  // blocks, rows of a part
+};
+
+Shape shape_of(int G, int64_t N, int sms) {
+  Shape s;
+  s.token = N * G <= kTokenRows;
+  s.rows = N * G <= 16 ? 16 : 32;
+  s.ctas = 2 * sms;
+  return s;
+}
+
+size_t part_bytes(const Shape& s, int d) {
+  return (size_t)s.ctas * 2 * s.rows * (d + kPartStats) * sizeof(float);
+}
+
+}  // namespace
+
 cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype,
                                 const int32_t* table, const int32_t* kv_len, const int32_t* q_len,
                                 void* o, float* lse, int B, int Hq, int64_t N, int max_pages,
                                 float scale, void* workspace, unsigned* status, int sms,
                                 cudaStream_t stream) {
-  const AttendParams p{q, {c.k_codes, c.v_codes}, {c.k_scale, c.v_scale}, table, kv_len, q_len, o,
-                       lse, status, N, c.num_pages, B, Hq, c.Hkv, Hq / c.Hkv, max_pages,
-                       page_log2(c.page), scale};
+  const Shape s = shape_of(Hq / c.Hkv, N, sms);
+  AttendParams p{q, {c.k_codes, c.v_codes}, {c.k_scale, c.v_scale}, table, kv_len, q_len, o,
+                 lse, status, N, c.num_pages, B, Hq, c.Hkv, Hq / c.Hkv, max_pages,
+                 page_log2(c.page), scale, static_cast<float*>(workspace), nullptr};
+  p.tails = reinterpret_cast<int4*>(static_cast<char*>(workspace) + part_bytes(s, c.d));
+  if (s.token) {
+    const cudaError_t e = launch_cache_token(p, c, dtype, (int)N * p.G, s.ctas, stream);
+    if (e != cudaSuccess) return e;
+    const JoinGeometry g{s.rows, 1, s.rows, (int)N, kTokenShift};
+    return launch_cache_join(p, g, dtype, c.d, s.ctas, stream);
+  }
   if (c.d == 64)
     return dtype == LA_BF16 ? attend_typed<__nv_bfloat16, 64>(p, stream)
                             : attend_typed<__half, 64>(p, stream);
@@ -90,6 +122,9 @@ cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype
                           : attend_typed<__half, 128>(p, stream);
 }
 
-size_t attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d, int sms) { return 256; }
+size_t attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d, int sms) {
+  const Shape s = shape_of(Hq / Hkv, N, sms);
+  return (part_bytes(s, d) + (size_t)s.ctas * sizeof(int4) + 255) / 256 * 256;
+}
 
 }  // namespace la

@@ -1,0 +1,604 @@
+// la_cache_token.cu -- attention of one or a few new tokens over the 8-bit cache.
+//
+// For the G query heads of a kv head and the n <= 32 / G tokens of a sequence,
+// R = n G rows in all, with codes c and page scales a (keys), b (values):
+//     s_rj = (q_r . c_j) a_j scale,   p_rj = exp(s_rj - m_r),   o_r = sum_j p_rj b_j c'_j / sum_j p_rj
+// over the cached tokens j that row r sees.  Each cached byte is used by R rows
+// only, 2 R flops a byte, so the cache's bytes from HBM bound it; the kernel is
+// built to keep copies in flight and to do little work for each byte.
+//
+// - A unit is a (sequence, kv head); its keys go by in tiles of 64 tokens.  One
+//   warp issues the tiles' bulk tensor copies (a page's rows of one head are
+//   contiguous; 128- or 64-byte swizzle so that the reads below meet no bank
+//   twice) through a ring of stages, on across unit boundaries.
+// - Four warps take 16 tokens of a tile each, with a running maximum, sum and
+//   output of their own, so nothing is exchanged until a unit ends.
+// - Codes become f16 in registers (exact), two for each conversion, straight in
+//   the layout of the products' operands: the sum over d may run in any
+//   order, so a lane's 16-byte pieces of a key row are its operand pieces of eight
+//   16-wide steps as they lie; for the values, pairs of tokens are put side
+//   by side by byte permutes.  No pass through shared memory.
+// - The products are mma.sync m16n8k16 (f16 in, fp32 sums): 16 rows at 2 R
+//   flops a byte are far from the tensor limits, and tcgen05 would need the
+//   converted tile in shared memory.
+// - q is scaled by a power of two for each row so that its largest entry lies in
+//   [2^14, 2^15) before it is rounded to f16: exact down to 2^-28 of the largest.
+// - Weights go to f16 as 2^15 p b_j / v, v the largest value scale so far
+//   (a power of two; the sums are rescaled when it or the maximum grows), so weights
+//   down to 2^-40 of the largest count.  Rounding them to f16 is 2^-11 each,
+//   of the size of the output's own rounding to fp16.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "la_cache.cuh"
+#include "la_ptx.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kTile = 64;        // tokens of a stage
+constexpr int kConsumers = 128;  // four warps
+constexpr int kThreads = kConsumers + 32;
+constexpr float kShift = kTokenShift;
+constexpr int kMinTokenTiles = 2;
+
+template <int D, int MT>
+struct TokenLayout {
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kStages = D == 128 ? (MT == 1 ? 5 : 4) : 8;
+  static constexpr int kHalf = kTile * D;             // bytes of a K or V tile
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kQOff = kStages * kStage;       // Q fragments
+  static constexpr int kBufOff = kQOff + MT * (D / 16) * 512;
+  static constexpr int kBuf = kRows * (D + 4) * 4;     // one fp32 output tile, rows padded
+  static constexpr int kStatOff = kBufOff + 2 * kBuf;  // wm[4][rows], wl[4][rows], wv[4], rs[rows]
+  static constexpr int kScaleOff = kStatOff + (9 * kRows + 4) * 4;  // float2 [stages][4]
+  static constexpr int kBarOff = (kScaleOff + kStages * 4 * 8 + 7) / 8 * 8;
+  static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;  // scan scratch, start, abort
+  static constexpr int kBytes = kMiscOff + 128 + 1024;        // + slack to align to 1024
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  ld_shared_v4(addr, v.x, v.y, v.z, v.w);
+  return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint64_t* bar, int c0,
+                                            int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// A block's walk along its share [pos, end) of the line of tiles.
+struct Walk {
+  int64_t pos, end;  // the share's next tile and its end
+  int b, h;          // unit of the next tile
+  int tile;          // its place in the unit
+  int tiles;         // tiles of the unit (0: sequence without work)
+  int kv, nq;        // its lengths
+
+  __device__ void load(const AttendParams& p) {
+    const int64_t len = p.kv_len[b], n = p.q_len ? (int64_t)p.q_len[b] : p.N;
+    const bool ok = attend_lengths_ok(len, n, p);
+    kv = (int)len;
+    nq = (int)n;
+    tiles = ok && n > 0 ? max(1, (int)((len + kTile - 1) / kTile)) : 0;
+  }
+  // the unit's tiles in this share: from `tile`, as many as returned
+  __device__ int count() const { return (int)min((int64_t)(tiles - tile), end - pos); }
+  // on to the next unit that has tiles (the share goes on)
+  __device__ void next(const AttendParams& p) {
+    pos += tiles - tile;
+    tile = 0;
+    if (++h < p.Hkv) return;
+    h = 0;
+    do {
+      ++b;
+      if (b >= p.B) return;
+      load(p);
+    } while (tiles == 0);
+  }
+};
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(kThreads, 2)
+    token_kernel(const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const AttendParams p, int box,
+                 int min_tiles) {
+  using L = TokenLayout<D, MT>;
+  constexpr int KS = D / 16;  // 16-wide steps of q . k
+  constexpr int NB = D / 8;   // 8-wide blocks of the output
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  float* buf = reinterpret_cast<float*>(sm + L::kBufOff);
+  float* wm = reinterpret_cast<float*>(sm + L::kStatOff);
+  float* wl = wm + 4 * L::kRows;
+  float* rs = wl + 4 * L::kRows;
+  float* wv = rs + L::kRows;
+  float2* sscale = reinterpret_cast<float2*>(sm + L::kScaleOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBarOff);
+  uint64_t* empty = full + L::kStages;
+  int64_t* misc = reinterpret_cast<int64_t*>(sm + L::kMiscOff);  // [0, 5) scan, then the start
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 12);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+
+  // The line's length, this block's share of it, and the unit where that begins.
+  Walk w;
+  int64_t total;
+  {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+    int64_t mine = 0;
+    for (w.b = b0; w.b < b1; ++w.b) {
+      w.load(p);
+      mine += (int64_t)w.tiles * p.Hkv;
+    }
+    int64_t before = block_exclusive_sum<kThreads>(mine, misc, total);
+    const int64_t shares = min((int64_t)gridDim.x, (total + min_tiles - 1) / min_tiles);
+    w.pos = w.end = 0;
+    if ((int64_t)blockIdx.x < shares) {
+      w.pos = total * blockIdx.x / shares;
+      w.end = total * (blockIdx.x + 1) / shares;
+    }
+    if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
+      for (w.b = b0;; ++w.b) {
+        w.load(p);
+        if (w.pos < before + (int64_t)w.tiles * p.Hkv) break;
+        before += (int64_t)w.tiles * p.Hkv;
+      }
+      misc[6] = w.b;
+      misc[7] = (w.pos - before) / w.tiles;
+      misc[8] = (w.pos - before) % w.tiles;
+    }
+    __syncthreads();
+    if (w.pos >= w.end) {
+      if (threadIdx.x == 0) p.tails[blockIdx.x] = make_int4(0, 0, 0, 0);
+      griddep_launch_dependents();
+      return;
+    }
+    w.b = (int)misc[6];
+    w.h = (int)misc[7];
+    w.tile = (int)misc[8];
+    w.load(p);
+  }
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ copies
+    // A lane knows the page and scales of 16 tokens: 32 lanes, eight tiles ahead.
+    if (lane == 0) {
+      prefetch_tmap(&map_k);
+      prefetch_tmap(&map_v);
+    }
+    const int per_box = box / 16;        // 16-token groups of a copy
+    const uint32_t bytes = (uint32_t)box * D;
+    int it = 0;
+    bool go = true;
+    while (w.pos < w.end && go) {
+      const int n = w.count();
+      const int* row = p.table + (int64_t)w.b * p.max_pages;
+      auto page_at = [&](int group) {  // page of 16-token group `group` of the unit (-2: none)
+        return (int64_t)group * 16 < w.kv ? row[group >> (p.page_log2 - 4)] : -2;
+      };
+      int ahead = page_at(w.tile * 4 + lane);
+      int id = -2;
+      float ks = 0.f, vs = 0.f;
+      for (int i = 0; i < n && go; ++i, ++it) {
+        const int t = w.tile + i;
+        if ((i & 7) == 0) {
+          id = ahead;
+          if (i + 8 < n) ahead = page_at((t + 8) * 4 + lane);
+          const bool known = id >= 0 && id < p.num_pages;
+          ks = -1.f;  // not a scale: the group's codes count as zero
+          vs = 0.f;
+          if (known) {
+            ks = __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + w.h);
+            vs = __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + w.h);
+          } else {
+            if (id != -2) atomicOr(p.status, kDevBadIndex);
+            id = -1;
+          }
+        }
+        const int s = it % L::kStages;
+        if (it >= L::kStages)
+          go = warp_wait(&empty[s], ((it / L::kStages) - 1) & 1, p.status, abort_flag);
+        if (!go) break;
+        const int g0 = (i & 7) * 4;  // first lane of this tile's groups
+        if (lane >= g0 && lane < g0 + 4) sscale[s * 4 + lane - g0] = make_float2(ks, vs);
+        const bool issue = lane >= g0 && lane < g0 + 4 && (lane & (per_box - 1)) == 0 && id >= 0;
+        const uint32_t copies = __popc(__ballot_sync(0xffffffffu, issue));
+        __syncwarp();
+        if (lane == 0) {
+          if (copies) mbar_arrive_expect_tx(&full[s], copies * 2 * bytes);
+          else mbar_arrive(&full[s]);
+        }
+        __syncwarp();
+        if (issue) {
+          const int at = (lane - g0) * 16;  // token of the tile
+          const int first = t * kTile + at;
+          const int64_t code_row = (((int64_t)id * p.Hkv + w.h) << p.page_log2) +
+                                   (first & ((1 << p.page_log2) - 1));
+          const uint32_t dst = base + s * L::kStage + at * D;
+          tma_load_2d(dst, &map_k, &full[s], 0, (int)code_row);
+          tma_load_2d(dst + L::kHalf, &map_v, &full[s], 0, (int)code_row);
+        }
+      }
+      if (go) w.next(p);
+    }
+    if (*abort_flag) {  // let copies already issued land before the block exits
+      for (int k = max(0, it - L::kStages); k < it; ++k)
+        mbar_wait_drain(&full[k % L::kStages], (k / L::kStages) & 1);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- products
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t sq = base + L::kQOff;
+  const T* qg = static_cast<const T*>(p.q);
+  int it = 0;
+  int4 tail = make_int4(0, 0, 0, 0);
+  bool ok = true;
+  while (w.pos < w.end && ok) {
+    const int n = w.count();
+    const int R = w.nq * p.G;
+    // q: rows as f16 operand pieces in shared memory, with each row's factor.
+    // Eight threads a row, D / 8 values each, two for each piece.
+    {
+      constexpr int V = D / 8;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 16 + (threadIdx.x >> 3), e = threadIdx.x & 7;
+        float x[V];
+        float top = 0.f;
+        if (r < R) {
+          const int i = r / p.G, head = w.h * p.G + r % p.G;
+          const T* src = qg + (((int64_t)w.b * p.Hq + head) * p.N + i) * D + e * V;
+#pragma unroll
+          for (int j = 0; j < V; j += 8) load8<T>(src + j, *reinterpret_cast<float(*)[8]>(x + j));
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) x[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+        for (int m = 4; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        // largest entry into [2^14, 2^15); rows of zeros, infinities and NaN as they are
+        const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+        const bool scaled = top > 0.f && ex < 128;
+        const int up = scaled ? min(14 - ex, 127) : 0;
+        const float f = scaled ? __uint_as_float((uint32_t)(max(up, -126) + 127) << 23) : 1.f;
+        if (e == 0) rs[r] = p.scale * kLog2e / f;
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+          const int d = e * V + j;
+          const int cc = d / (D / 4), ks = (d % (D / 4)) / 4, pair = (d & 3) >> 1;
+          const uint32_t at = sq + (((mt * KS + ks) * 32 + (r & 7) * 4 + cc) * 16) +
+                              (pair * 2 + ((r >> 3) & 1)) * 4;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack2<__half>(x[j] * f, x[j + 1] * f))
+                       : "memory");
+        }
+      }
+    }
+    named_barrier_sync(1, kConsumers);
+
+    float o[MT][NB][4], m[MT][2], l[MT][2], rf[MT][2];
+    int last[MT][2];  // last token that the row sees
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = mt * 16 + k * 8 + g;
+        m[mt][k] = -INFINITY;
+        l[mt][k] = 0.f;
+        rf[mt][k] = rs[r];
+        last[mt][k] = r < R ? w.kv - w.nq + r / p.G : w.kv - 1;
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[mt][j][k] = 0.f;
+    }
+    float vref = 0.f, vinv = 0.f;
+
+    for (int i = 0; i < n; ++i, ++it) {
+      const int s = it % L::kStages;
+      ok = warp_wait(&full[s], (it / L::kStages) & 1, p.status, abort_flag);
+      if (!ok) break;
+      const int t0 = (w.tile + i) * kTile + warp * 16;  // first of this warp's 16 tokens
+      if (t0 >= w.kv) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        continue;
+      }
+      const float2 sc = sscale[s * 4 + warp];
+      const uint32_t kb = base + s * L::kStage + warp * 16 * D, vb = kb + L::kHalf;
+      // scores: 16 rows x 16 tokens for each row block
+      float sr[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sr[mt][nb][k] = 0.f;
+      uint32_t kw[2][KS];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+        const int row = nb * 8 + g;  // of the warp's 16 (a multiple of 8 rows into the tile)
+        if constexpr (D == 128) {
+          const uint4 x = lds128(kb + row * D + (((2 * c) ^ g) << 4));
+          const uint4 y = lds128(kb + row * D + (((2 * c + 1) ^ g) << 4));
+          kw[nb][0] = x.x; kw[nb][1] = x.y; kw[nb][2] = x.z; kw[nb][3] = x.w;
+          kw[nb][4] = y.x; kw[nb][5] = y.y; kw[nb][6] = y.z; kw[nb][7] = y.w;
+        } else {
+          const uint4 x = lds128(kb + row * D + ((c ^ ((g >> 1) & 3)) << 4));
+          kw[nb][0] = x.x; kw[nb][1] = x.y; kw[nb][2] = x.z; kw[nb][3] = x.w;
+        }
+      }
+      // values: tokens 2c, 2c + 1, 2c + 8, 2c + 9, D / 8 numbers each from (D / 8) g on
+      uint32_t vw[4][D / 32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = 2 * c + (k & 1) + (k >> 1) * 8;
+        if constexpr (D == 128) {
+          const uint4 x = lds128(vb + row * D + ((g ^ (row & 7)) << 4));
+          vw[k][0] = x.x; vw[k][1] = x.y; vw[k][2] = x.z; vw[k][3] = x.w;
+        } else {
+          const uint2 x = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+          vw[k][0] = x.x; vw[k][1] = x.y;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      const bool edge = t0 + 16 > w.kv || sc.x < 0.f;  // rows of the tile that hold no token
+      if (edge) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (sc.x < 0.f || t0 + 2 * c + (k & 1) + (k >> 1) * 8 >= w.kv)
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) vw[k][j] = 0u;
+        if (sc.x < 0.f)
+#pragma unroll
+          for (int j = 0; j < KS; ++j) kw[0][j] = kw[1][j] = 0u;
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t kf[2][2];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          kf[nb][0] = e4m3x2_to_f16x2(kw[nb][ks] & 0xffffu);
+          kf[nb][1] = e4m3x2_to_f16x2(kw[nb][ks] >> 16);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint4 a = lds128(sq + ((mt * KS + ks) * 32 + lane) * 16);
+          mma16816(sr[mt][0], a, kf[0][0], kf[0][1]);
+          mma16816(sr[mt][1], a, kf[1][0], kf[1][1]);
+        }
+      }
+      // value scales: a larger one than before makes the sums relative to it
+      float grow = 1.f;
+      if (sc.y > vref) {
+        grow = vref / sc.y;
+        vref = sc.y;
+        vinv = 1.f / vref;
+      }
+      const float vf = sc.y * vinv;
+      const float kf = fmaxf(sc.x, 0.f);
+      const bool hidden = t0 + 15 > w.kv - w.nq;  // some row does not see some token
+      uint4 pa[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float pr[2][4], a[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float f = rf[mt][k] * kf;
+          float mx = m[mt][k];
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float x = sr[mt][nb][2 * k + j] * f;
+              if (hidden && t0 + nb * 8 + 2 * c + j > last[mt][k]) x = -INFINITY;
+              pr[nb][2 * k + j] = x;
+              mx = fmaxf(mx, x);
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          a[k] = exp2_fast(m[mt][k] - ref);
+          m[mt][k] = mx;
+          float sum = 0.f;
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float e = exp2_fast(pr[nb][2 * k + j] - ref + kShift);
+              sum += e;
+              pr[nb][2 * k + j] = e * vf;
+            }
+          l[mt][k] = l[mt][k] * a[k] + sum;
+          a[k] *= grow;
+        }
+        pa[mt] = make_uint4(pack2<__half>(pr[0][0], pr[0][1]), pack2<__half>(pr[0][2], pr[0][3]),
+                            pack2<__half>(pr[1][0], pr[1][1]), pack2<__half>(pr[1][2], pr[1][3]));
+        if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            o[mt][j][0] *= a[0];
+            o[mt][j][1] *= a[0];
+            o[mt][j][2] *= a[1];
+            o[mt][j][3] *= a[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const uint32_t t01a = __byte_perm(vw[0][j], vw[1][j], 0x5140);
+        const uint32_t t01b = __byte_perm(vw[0][j], vw[1][j], 0x7362);
+        const uint32_t t23a = __byte_perm(vw[2][j], vw[3][j], 0x5140);
+        const uint32_t t23b = __byte_perm(vw[2][j], vw[3][j], 0x7362);
+        const uint32_t b0[4] = {e4m3x2_to_f16x2(t01a & 0xffffu), e4m3x2_to_f16x2(t01a >> 16),
+                                e4m3x2_to_f16x2(t01b & 0xffffu), e4m3x2_to_f16x2(t01b >> 16)};
+        const uint32_t b1[4] = {e4m3x2_to_f16x2(t23a & 0xffffu), e4m3x2_to_f16x2(t23a >> 16),
+                                e4m3x2_to_f16x2(t23b & 0xffffu), e4m3x2_to_f16x2(t23b >> 16)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * j + k], pa[mt], b0[k], b1[k]);
+      }
+    }
+    if (!ok) break;
+
+    // the four warps' parts of the unit into one
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 1);
+        l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 2);
+        if (c == 0) {
+          wm[warp * L::kRows + mt * 16 + k * 8 + g] = m[mt][k];
+          wl[warp * L::kRows + mt * 16 + k * 8 + g] = l[mt][k];
+        }
+      }
+    if (lane == 0) wv[warp] = vref;
+    named_barrier_sync(1, kConsumers);
+    const float vmax = fmaxf(fmaxf(wv[0], wv[1]), fmaxf(wv[2], wv[3]));
+    auto row_max = [&](int r) {
+      return fmaxf(fmaxf(wm[r], wm[L::kRows + r]), fmaxf(wm[2 * L::kRows + r], wm[3 * L::kRows + r]));
+    };
+    const float vpart = vmax > 0.f ? vref / vmax : 0.f;
+    auto each = [&](auto&& f) {  // f(row, column, value) over this thread's part
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = mt * 16 + k * 8 + g;
+          const float mx = row_max(r);
+          const float a = exp2_fast(m[mt][k] - (mx == -INFINITY ? 0.f : mx)) * vpart;
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+            for (int j = 0; j < NB; j += 4)
+              f(buf + (warp & 1) * (L::kBuf / 4) + r * (D + 4) + (2 * c + jj) * NB + j,
+                make_float4(o[mt][j][2 * k + jj] * a, o[mt][j + 1][2 * k + jj] * a,
+                            o[mt][j + 2][2 * k + jj] * a, o[mt][j + 3][2 * k + jj] * a));
+        }
+    };
+    if (warp >= 2) each([](float* at, float4 x) { *reinterpret_cast<float4*>(at) = x; });
+    named_barrier_sync(1, kConsumers);
+    if (warp < 2)
+      each([](float* at, float4 x) {
+        float4* y = reinterpret_cast<float4*>(at);
+        const float4 z = *y;
+        *y = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
+      });
+    named_barrier_sync(1, kConsumers);
+    const bool begins = w.tile == 0, ends = w.tile + n == w.tiles;
+    float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * L::kRows * (D + kPartStats);
+    for (int e = threadIdx.x; e < R * (D / 4); e += kConsumers) {
+      const int r = e / (D / 4), d4 = e % (D / 4);
+      const float4 x = *reinterpret_cast<float4*>(buf + r * (D + 4) + d4 * 4);
+      const float4 y = *reinterpret_cast<float4*>(buf + L::kBuf / 4 + r * (D + 4) + d4 * 4);
+      float4 z = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      const float mx = row_max(r), ref = mx == -INFINITY ? 0.f : mx;
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum += wl[k * L::kRows + r] * exp2_fast(wm[k * L::kRows + r] - ref);
+      if (begins && ends) {
+        const int i = r / p.G, head = w.h * p.G + r % p.G;
+        const int64_t row = ((int64_t)w.b * p.Hq + head) * p.N + i;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+        uint2 out;
+        out.x = pack2<T>(z.x * inv * vmax, z.y * inv * vmax);
+        out.y = pack2<T>(z.z * inv * vmax, z.w * inv * vmax);
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + row * D + d4 * 4) = out;
+        if (p.lse && d4 == 0) p.lse[row] = (mx - kShift + log2f(sum)) * kLn2;
+      } else {
+        reinterpret_cast<float4*>(part)[r * (D / 4) + d4] = z;
+        if (d4 == 0)
+          reinterpret_cast<float4*>(part + L::kRows * D)[r] = make_float4(mx, sum, vmax, 0.f);
+      }
+    }
+    if (begins && !ends) {
+      // blocks that hold the rest: the share of block k ends at total (k + 1) / shares
+      const int64_t unit_end = w.pos + w.tiles;
+      const int64_t shares = min((int64_t)gridDim.x, (total + min_tiles - 1) / min_tiles);
+      int k = blockIdx.x;
+      while (total * (k + 1) / shares < unit_end) ++k;
+      tail = make_int4(k - (int)blockIdx.x, w.b, w.h, 0);
+    }
+    named_barrier_sync(1, kConsumers);
+    w.next(p);
+  }
+  if (threadIdx.x == 0) p.tails[blockIdx.x] = ok ? tail : make_int4(0, 0, 0, 0);
+  griddep_launch_dependents();
+}
+
+template <typename T, int D, int MT>
+cudaError_t launch_typed(const AttendParams& p, const CUtensorMap& k, const CUtensorMap& v, int box,
+                         int ctas, cudaStream_t stream) {
+  constexpr int bytes = TokenLayout<D, MT>::kBytes;
+  static_assert(bytes <= 113 * 1024, "two blocks for each SM");
+  auto* kernel = token_kernel<T, D, MT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, kThreads, bytes, stream>>>(k, v, p, box, kMinTokenTiles);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const AttendParams& p, const CUtensorMap& k, const CUtensorMap& v, int box,
+                        int rows, int ctas, cudaStream_t stream) {
+  return rows <= 16 ? launch_typed<T, D, 1>(p, k, v, box, ctas, stream)
+                    : launch_typed<T, D, 2>(p, k, v, box, ctas, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_token(const AttendParams& p, const la_cache& c, la_dtype dtype, int rows,
+                               int ctas, cudaStream_t stream) {
+  CUtensorMap k, v;
+  const int box = std::min(c.page, kTile);
+  if (!make_tmap_codes(&k, c.k_codes, c.num_pages * c.Hkv * c.page, c.d, box) ||
+      !make_tmap_codes(&v, c.v_codes, c.num_pages * c.Hkv * c.page, c.d, box))
+    return cudaErrorInvalidValue;
+  if (c.d == 64)
+    return dtype == LA_BF16 ? launch_rows<__nv_bfloat16, 64>(p, k, v, box, rows, ctas, stream)
+                            : launch_rows<__half, 64>(p, k, v, box, rows, ctas, stream);
+  return dtype == LA_BF16 ? launch_rows<__nv_bfloat16, 128>(p, k, v, box, rows, ctas, stream)
+                          : launch_rows<__half, 128>(p, k, v, box, rows, ctas, stream);
+}
+
+}  // namespace la

@@ -47,6 +47,9 @@ la_status check_prefill_ptrs(const void* q, const void* k, const void* v, const 
 // Builds a 3-D bf16 tensor map; returns false on failure.
 bool make_tmap_bf16(CUtensorMap* map, const void* base, int64_t rows_per_head, int64_t heads,
                     int box_rows);
+// 2-D map over rows of d 8-bit codes (d = 64 or 128, swizzled by d bytes), boxes
+// of box_rows rows.
+bool make_tmap_codes(CUtensorMap* map, const void* base, int64_t rows, int d, int box_rows);
 // 3-D fp32 tensor map over `units` d x d states [units, 128, 128]; box
 // {32, 128, 1} (32 columns of one state), 128-byte swizzle.
 bool make_tmap_state(CUtensorMap* map, const void* base, int64_t units);
