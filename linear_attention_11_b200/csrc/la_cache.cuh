@@ -18,6 +18,8 @@ struct AttendParams;
 struct JoinGeometry;
 cudaError_t launch_cache_token(const AttendParams& p, const la_cache& c, la_dtype dtype, int rows,
                                int ctas, cudaStream_t stream);
+cudaError_t launch_cache_prompt(const AttendParams& p, la_dtype dtype, int d, int ctas,
+                                cudaStream_t stream);
 cudaError_t launch_cache_join(const AttendParams& p, const JoinGeometry& g, la_dtype dtype, int d,
                               int ctas, cudaStream_t stream);
 
@@ -175,7 +177,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-constexpr float kTokenShift = 15.f;  // weights of the token kernel are 2^15 at the maximum
+// Weights are held as 2^shift at a row's reference maximum.
+constexpr float kTokenShift = 15.f, kPromptShift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -56,7 +56,7 @@ struct TokenLayout {
   static constexpr int kStatOff = kBufOff + 2 * kBuf;  // wm[4][rows], wl[4][rows], wv[4], rs[rows]
   static constexpr int kScaleOff = kStatOff + (9 * kRows + 4) * 4;  // float2 [stages][4]
   static constexpr int kBarOff = (kScaleOff + kStages * 4 * 8 + 7) / 8 * 8;
-  static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;  // scan scratch, start, abort
+  static constexpr int kMiscOff = kBarOff + (2 * kStages + 1) * 8;  // scan scratch, start, abort
   static constexpr int kBytes = kMiscOff + 128 + 1024;        // + slack to align to 1024
 };
 
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float2* sscale = reinterpret_cast<float2*>(sm + L::kScaleOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBarOff);
   uint64_t* empty = full + L::kStages;
+  uint64_t* consumers = empty + L::kStages;  // a barrier of the four warps
   int64_t* misc = reinterpret_cast<int64_t*>(sm + L::kMiscOff);  // [0, 5) scan, then the start
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 12);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 4);
     }
+    mbar_init(consumers, 4);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -265,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int g = lane >> 2, c = lane & 3;
   const uint32_t sq = base + L::kQOff;
   const T* qg = static_cast<const T*>(p.q);
-  int it = 0;
+  int it = 0, syncs = 0;
+  auto sync = [&]() { return warps_sync(consumers, syncs, p.status, abort_flag); };
   int4 tail = make_int4(0, 0, 0, 0);
   bool ok = true;
   while (w.pos < w.end && ok) {
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-    named_barrier_sync(1, kConsumers);
+    if (!(ok = sync())) break;
 
     float o[MT][NB][4], m[MT][2], l[MT][2], rf[MT][2];
     int last[MT][2];  // last token that the row sees
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     if (lane == 0) wv[warp] = vref;
-    named_barrier_sync(1, kConsumers);
+    if (!(ok = sync())) break;
     const float vmax = fmaxf(fmaxf(wv[0], wv[1]), fmaxf(wv[2], wv[3]));
     auto row_max = [&](int r) {
       return fmaxf(fmaxf(wm[r], wm[L::kRows + r]), fmaxf(wm[2 * L::kRows + r], wm[3 * L::kRows + r]));
@@ -517,14 +520,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     };
     if (warp >= 2) each([](float* at, float4 x) { *reinterpret_cast<float4*>(at) = x; });
-    named_barrier_sync(1, kConsumers);
+    if (!(ok = sync())) break;
     if (warp < 2)
       each([](float* at, float4 x) {
         float4* y = reinterpret_cast<float4*>(at);
         const float4 z = *y;
         *y = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
       });
-    named_barrier_sync(1, kConsumers);
+    if (!(ok = sync())) break;
     const bool begins = w.tile == 0, ends = w.tile + n == w.tiles;
     float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * L::kRows * (D + kPartStats);
     for (int e = threadIdx.x; e < R * (D / 4); e += kConsumers) {
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       while (total * (k + 1) / shares < unit_end) ++k;
       tail = make_int4(k - (int)blockIdx.x, w.b, w.h, 0);
     }
-    named_barrier_sync(1, kConsumers);
+    if (!(ok = sync())) break;
     w.next(p);
   }
   if (threadIdx.x == 0) p.tails[blockIdx.x] = ok ? tail : make_int4(0, 0, 0, 0);

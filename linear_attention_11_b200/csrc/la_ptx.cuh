@@ -100,6 +100,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
   return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;
 }
 
+// A barrier of some of a block's warps, each taking part with all its lanes:
+// `bar` counts one arrival a warp, `phase` is the caller's count of its syncs.
+// Bounded like mbar_wait (a bar.sync would wait for good for a warp that gave up).
+__device__ __forceinline__ bool warps_sync(uint64_t* bar, int& phase, unsigned* status,
+                                           volatile int* abort) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  const bool ok = warp_wait(bar, phase & 1, status, abort);
+  ++phase;
+  return ok;
+}
+
 // Plain bounded wait used only while tearing down after an abort: waits for
 // copies already in flight to land so the block never exits under them.
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {

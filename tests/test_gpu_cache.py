@@ -441,6 +441,28 @@ def test_two_streams_at_once(la):
     clean(la)
 
 
+@pytest.mark.parametrize("d,G", [(64, 3), (128, 4)])
+def test_many_short_units_for_each_block(la, d, G):
+    """Ragged prompts of several users: a block works on three units and more, some of one key tile."""
+    nq = [777, 400, 130, 61, 700, 256]
+    kv = [n + past for n, past in zip(nq, [0, 37, 600, 300, 128, 0])]
+    cache, table = filled_cache(kv, 4, 32, d, 20)
+    q = normal(4, 6, 4 * G, 777, d).half()
+    for b, n in enumerate(nq):   # the oracle takes some rows of each sequence
+        q[b, :, n:] = 0
+    dev, t = to_device(la, cache, DEV), torch.from_numpy(table).to(DEV)
+    lse = torch.zeros(q.shape[:3], device=DEV)
+    o = la.la_cache_attend(q.to(DEV), dev, t, ints(kv, DEV), q_len=ints(nq, DEV), lse=lse)
+    for b, n in enumerate(nq):
+        rows = sorted({0, 1, n - 1, n // 2, *range(40, n, 97)})
+        for i in rows:
+            ref = oc.attend(cache, table[b:b + 1], q[b:b + 1, :, i:i + 1].double().numpy(),
+                            [kv[b] - n + i + 1], [1], d ** -0.5)
+            assert_attend(o[b:b + 1, :, i:i + 1], lse[b:b + 1, :, i:i + 1], ref, kv[b], d, q.dtype,
+                          f"sequence {b} row {i}")
+    clean(la)
+
+
 def test_a_large_batch(la):
     """More sequences than SMs, lengths all different."""
     B, d, page = 300, 64, 16
