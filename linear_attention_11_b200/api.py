@@ -134,8 +134,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle itself: torch.cuda.current_stream() costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -371,70 +371,103 @@ def la_decode_steps(S, q, k, v, o=None, stream=None):
     return o
 
 
+# The cache calls check a dozen tensors, and a decode step is some microseconds
+# long: one expression sees whether all is well (_cache_fits), and only a call
+# that is not goes through the checks that say what is wrong.
+def _cache_fits(cache, table, lengths, tensors):
+    kc, vc, ks, vs = cache
+    dev, e4m3, f32, i32 = kc.get_device(), torch.float8_e4m3fn, torch.float32, torch.int32
+    pages, B = kc.shape[:2], table.shape[0]
+    if not (dev >= 0 and dev == torch.cuda.current_device() and kc.dtype == e4m3
+            and vc.dtype == e4m3 and ks.dtype == f32 and vs.dtype == f32 and table.dtype == i32
+            and kc.dim() == 4
+            and vc.shape == kc.shape and ks.shape == pages and vs.shape == pages
+            and table.dim() == 2 and kc.is_contiguous() and vc.is_contiguous()
+            and ks.is_contiguous() and vs.is_contiguous() and table.is_contiguous()
+            and vc.get_device() == dev and ks.get_device() == dev and vs.get_device() == dev
+            and table.get_device() == dev):
+        return False
+    for t in lengths:
+        if t is not None and not (t.dtype == i32 and t.get_device() == dev and t.dim() == 1
+                                  and t.shape[0] == B and t.is_contiguous()):
+            return False
+    for t in tensors:
+        if t is not None and not (t.get_device() == dev and t.is_contiguous()):
+            return False
+    return True
+
+
 def _cache(fn, cache, table, lengths, tensors):
-    """The C view of a cache after checks of it, of the page table, of the int32
-    [B] arrays `lengths` (None allowed) and of the devices of all of them."""
-    kc = cache.k_codes
-    for name in ("k_codes", "v_codes"):
-        _need(fn, name, getattr(cache, name), torch.float8_e4m3fn)
-    for name in ("k_scale", "v_scale"):
-        _need(fn, name, getattr(cache, name), torch.float32)
-    if (kc.dim() != 4 or cache.v_codes.shape != kc.shape or cache.k_scale.shape != kc.shape[:2]
-            or cache.v_scale.shape != kc.shape[:2]):
-        raise ValueError(f"{fn}: expected codes [num_pages,Hkv,page,d] and scales [num_pages,Hkv]; "
-                         f"got {[tuple(t.shape) for t in cache]}")
-    _need(fn, "table", table, torch.int32)
-    if table.dim() != 2:
-        raise ValueError(f"{fn}: table must be [B,max_pages], not {tuple(table.shape)}")
-    for name, t in lengths.items():
-        _need(fn, name, t, torch.int32)
-        if t is not None and tuple(t.shape) != (table.shape[0],):
-            raise ValueError(f"{fn}: {name} must be [{table.shape[0]}], not {tuple(t.shape)}")
-    dev = kc.device
-    for t in (*cache, table, *lengths.values(), *tensors):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{fn}: tensors on {dev} and on {t.device}")
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: tensors on {dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    """The C view of a cache after checks of it, of the page table, of the int32 [B]
+    arrays in the dict `lengths` and of the other tensors in `tensors` (a dict, None allowed in both)."""
+    kc, vc, ks, vs = cache
+    if not _cache_fits(cache, table, lengths.values(), tensors.values()):
+        for name in ("k_codes", "v_codes"):
+            _need(fn, name, getattr(cache, name), torch.float8_e4m3fn)
+        for name in ("k_scale", "v_scale"):
+            _need(fn, name, getattr(cache, name), torch.float32)
+        if (kc.dim() != 4 or vc.shape != kc.shape or ks.shape != kc.shape[:2]
+                or vs.shape != kc.shape[:2]):
+            raise ValueError(f"{fn}: expected codes [num_pages,Hkv,page,d] and scales "
+                             f"[num_pages,Hkv]; got {[tuple(t.shape) for t in cache]}")
+        _need(fn, "table", table, torch.int32)
+        if table.dim() != 2:
+            raise ValueError(f"{fn}: table must be [B,max_pages], not {tuple(table.shape)}")
+        for name, t in lengths.items():
+            _need(fn, name, t, torch.int32)
+            if t is not None and tuple(t.shape) != (table.shape[0],):
+                raise ValueError(f"{fn}: {name} must be [{table.shape[0]}], not {tuple(t.shape)}")
+        for name, t in tensors.items():
+            _need(fn, name, t)
+        dev = kc.device
+        for t in (*cache, table, *lengths.values(), *tensors.values()):
+            if t is not None and t.device != dev:
+                raise ValueError(f"{fn}: tensors on {dev} and on {t.device}")
+        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            raise ValueError(f"{fn}: tensors on {dev}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
     P, Hkv, page, d = kc.shape
-    return _la_cache(kc.data_ptr(), cache.v_codes.data_ptr(), cache.k_scale.data_ptr(),
-                     cache.v_scale.data_ptr(), P, Hkv, page, d)
+    return _la_cache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, Hkv, page, d)
 
 
-def _cache_kv(fn, cache, table, k, v):
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cache_kv(fn, c, table, k, v):
     """k, v [B,Hkv,N,d] of one of the three types that fit the cache and the table -> (dtype, N)."""
-    _need(fn, "k", k)
-    _need(fn, "v", v)
-    P, Hkv, page, d = cache.k_codes.shape
-    if (k.dim() != 4 or k.shape != v.shape or tuple(k.shape[:2]) != (table.shape[0], Hkv)
-            or k.shape[3] != d):
-        raise ValueError(f"{fn}: expected k, v [{table.shape[0]},{Hkv},N,{d}]; got k "
+    shape = k.shape
+    if (len(shape) != 4 or shape != v.shape or shape[0] != table.shape[0] or shape[1] != c.Hkv
+            or shape[3] != c.d):
+        raise ValueError(f"{fn}: expected k, v [{table.shape[0]},{c.Hkv},N,{c.d}]; got k "
                          f"{tuple(k.shape)}, v {tuple(v.shape)}")
-    if k.dtype != v.dtype or k.dtype not in DTYPES:
+    dtype = DTYPES.get(k.dtype)
+    if dtype is None or k.dtype != v.dtype:
         raise ValueError(f"{fn}: k and v must be of one type, bfloat16, float16 or float32, not "
                          f"{k.dtype} and {v.dtype}")
-    return DTYPES[k.dtype], k.shape[2]
+    return dtype, shape[2]
 
 
 def la_cache_write(k, v, cache: la_cache, table, start, count=None, stream=None):
     """Store tokens start[b] + i, i < count[b] (or N), from k, v [B,Hkv,N,d] (bf16, fp16
     or fp32, CUDA) in the pages table [B,max_pages]; start, count int32 [B]."""
-    c = _cache("la_cache_write", cache, table, {"start": start, "count": count}, (k, v))
-    dtype, N = _cache_kv("la_cache_write", cache, table, k, v)
+    c = _cache("la_cache_write", cache, table, {"start": start, "count": count}, {"k": k, "v": v})
+    dtype, N = _cache_kv("la_cache_write", c, table, k, v)
+    B, max_pages = table.shape
     _check("la_cache_write", load_library().la_cache_write(
-        _ptr(k), _ptr(v), dtype, ctypes.byref(c), _ptr(table), _ptr(start), _ptr(count),
-        table.shape[0], N, table.shape[1], _stream(stream)))
+        k.data_ptr(), v.data_ptr(), dtype, c, table.data_ptr(), _address(start), _address(count), B,
+        N, max_pages, _stream(stream)))
 
 
 def la_cache_read(cache: la_cache, table, start, k, v, count=None, stream=None):
     """Tokens start[b] + i, i < count[b] (or N), into k, v [B,Hkv,N,d] (bf16, fp16 or
     fp32, CUDA), which are returned."""
-    c = _cache("la_cache_read", cache, table, {"start": start, "count": count}, (k, v))
-    dtype, N = _cache_kv("la_cache_read", cache, table, k, v)
+    c = _cache("la_cache_read", cache, table, {"start": start, "count": count}, {"k": k, "v": v})
+    dtype, N = _cache_kv("la_cache_read", c, table, k, v)
+    B, max_pages = table.shape
     _check("la_cache_read", load_library().la_cache_read(
-        ctypes.byref(c), _ptr(table), _ptr(start), _ptr(count), _ptr(k), _ptr(v), dtype,
-        table.shape[0], N, table.shape[1], _stream(stream)))
+        c, table.data_ptr(), _address(start), _address(count), k.data_ptr(), v.data_ptr(), dtype, B,
+        N, max_pages, _stream(stream)))
     return k, v
 
 
@@ -449,32 +482,35 @@ def la_cache_attend(q, cache: la_cache, table, kv_len, q_len=None, o=None, lse=N
     defaults to 1/sqrt(d).  With a workspace (CUDA, contiguous) the call is
     la_cache_attend_ws."""
     fn = "la_cache_attend" if workspace is None else "la_cache_attend_ws"
-    c = _cache(fn, cache, table, {"kv_len": kv_len, "q_len": q_len}, (q, o, lse, workspace))
-    _need(fn, "q", q)
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"{fn}: q must be bfloat16 or float16, not {q.dtype}")
-    _need(fn, "o", o, q.dtype)
-    _need(fn, "lse", lse, torch.float32)
-    _need(fn, "workspace", workspace)
-    if (q.dim() != 4 or q.shape[0] != table.shape[0] or q.shape[3] != c.d
-            or (o is not None and o.shape != q.shape)):
+    c = _cache(fn, cache, table, {"kv_len": kv_len, "q_len": q_len},
+               {"q": q, "o": o, "lse": lse, "workspace": workspace})
+    dtype, shape = q.dtype, q.shape
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise ValueError(f"{fn}: q must be bfloat16 or float16, not {dtype}")
+    if o is not None and o.dtype != dtype:
+        raise ValueError(f"{fn}: o must be {dtype}, not {o.dtype}")
+    if (len(shape) != 4 or shape[0] != table.shape[0] or shape[3] != c.d
+            or (o is not None and o.shape != shape)):
         raise ValueError(f"{fn}: expected q, o [{table.shape[0]},Hq,N,{c.d}]; got q "
-                         f"{tuple(q.shape)}" + ("" if o is None else f", o {tuple(o.shape)}"))
-    if lse is not None and lse.shape != q.shape[:3]:
-        raise ValueError(f"{fn}: lse must be {list(q.shape[:3])}, not {tuple(lse.shape)}")
+                         f"{tuple(shape)}" + ("" if o is None else f", o {tuple(o.shape)}"))
+    if lse is not None:
+        if lse.dtype != torch.float32:
+            raise ValueError(f"{fn}: lse must be torch.float32, not {lse.dtype}")
+        if lse.shape != shape[:3]:
+            raise ValueError(f"{fn}: lse must be {list(shape[:3])}, not {tuple(lse.shape)}")
     if kv_len is None:
         raise ValueError(f"{fn}: kv_len is required")
-    B, Hq, N, d = q.shape
+    B, Hq, N, d = shape
     if o is None:
         o = torch.empty_like(q)
-    args = (_ptr(q), DTYPES[q.dtype], ctypes.byref(c), _ptr(table), _ptr(kv_len), _ptr(q_len),
-            _ptr(o), _ptr(lse), B, Hq, N, table.shape[1],
+    args = (q.data_ptr(), DTYPES[dtype], c, table.data_ptr(), kv_len.data_ptr(), _address(q_len),
+            o.data_ptr(), _address(lse), B, Hq, N, table.shape[1],
             1.0 / math.sqrt(d) if scale is None else scale)
     if workspace is None:
         _check(fn, load_library().la_cache_attend(*args, _stream(stream)))
     else:
         nbytes = workspace.numel() * workspace.element_size()
-        _check(fn, load_library().la_cache_attend_ws(*args, _ptr(workspace), nbytes,
+        _check(fn, load_library().la_cache_attend_ws(*args, workspace.data_ptr(), nbytes,
                                                      _stream(stream)))
     return o
 

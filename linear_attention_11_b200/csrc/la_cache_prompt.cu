@@ -9,15 +9,15 @@
 // for a key tile each, so the two 128-row tiles take turns: one's products run
 // under the other's softmax.
 //
-// Roles (416 threads, one block for each SM):
+// Roles (640 threads, one block for each SM):
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread owns a row (= a lane of
 //                   tensor memory), so maxima and sums need no exchange; q to f16
 //                   and its row factor at a unit's start; output at its end
-//   warps 8-11      codes to f16 in shared memory, 128-byte swizzled as the
+//   warps 8-15      codes to f16 in shared memory, 128-byte swizzled as the
 //                   products read them: pages are gathered by plain 16-byte loads one
 //                   half tile ahead, as the conversion needs the codes in registers
 //                   anyway
-//   warp 12         issues the products
+//   warp 16         issues the products (17 to 19 fill up its warpgroup: registers go by those)
 // The scale of a page against the largest of the block's share of the unit is a
 // power of two and goes into the conversion (exact in f16 down to 2^-15 of the
 // largest; below, codes lose bits that weigh 2^-24 of it), so one factor a row is
@@ -36,10 +36,14 @@ namespace la {
 namespace {
 
 constexpr int kKeys = 128;  // tokens of a key tile
-constexpr int kThreads = 416;
+constexpr int kThreads = 640, kConvert = 256;
+constexpr int kIssue = 16;  // the warp that issues the products
 constexpr float kShift = kPromptShift;
 constexpr float kSlack = 8.f;  // growth of a row's maximum that is let pass
 constexpr int kMinTiles = 2;
+// registers of a thread after the split; 640 x 96 at launch
+constexpr int kRegsSoftmax = 136, kRegsConvert = 80, kRegsIssue = 40;
+static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= 640 * 96, "registers");
 
 template <int D>
 struct PromptLayout {
@@ -48,11 +52,12 @@ struct PromptLayout {
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kSlotOff = 2 * kQ;
   static constexpr int kMiscOff = kSlotOff + kSlots * kSlot;
-  // scan scratch 13 x 8, start 4 x 8 | barriers | e values, reductions
+  // scan scratch 20 x 8, start 3 x 8, line and shares 2 x 8 | walks | barriers | e values
   static constexpr int kBars = 2 * kSlots + 2 * 6 + 2;
-  static constexpr int kBarOff = kMiscOff + 160;
-  static constexpr int kEOff = kBarOff + kBars * 8;  // float2 e[2], float2 red[4]
-  static constexpr int kEnd = kEOff + 48 + 16;       // tmem slot, abort flag
+  static constexpr int kWalkOff = kMiscOff + 208;
+  static constexpr int kBarOff = kWalkOff + 17 * 64;
+  static constexpr int kEOff = kBarOff + kBars * 8;  // float2 e[2], float2 red[8]
+  static constexpr int kEnd = kEOff + 80 + 16;       // tmem slot, abort flag
   static constexpr int kBytes = kEnd + 1024;
 };
 
@@ -61,7 +66,9 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
          ((uint32_t)(M >> 4) << 24);
 }
 
-// A block's walk along its share of the line of key tiles: units (b, h, qt).
+// A block's walk along its share of the line of key tiles: units (b, h, qt).  Each
+// warp has one in shared memory, which its lane 0 moves on: in registers it would
+// crowd out the score rows.
 struct Walk {
   int64_t pos, end;
   int b, h, qt;
@@ -104,6 +111,30 @@ struct Walk {
   }
 };
 
+// 16 bytes, or zeros.  Volatile, so that the loads stay where they are written:
+// ahead of the conversion before them.
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)there));
+  return v;
+}
+
+// A word, or `other`, likewise.
+__device__ __forceinline__ int load_word(const int* p, bool there, int other) {
+  int v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\tmov.b32 %0, %3;\n\t"
+      "@q ld.global.nc.b32 %0, [%1];\n\t}"
+      : "=&r"(v)
+      : "l"(p), "r"((uint32_t)there), "r"(other));
+  return v;
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 f) {
   const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), f);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -118,6 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
   int64_t* misc = reinterpret_cast<int64_t*>(sm + L::kMiscOff);
+  Walk* walks = reinterpret_cast<Walk*>(sm + L::kWalkOff);
+  static_assert(sizeof(Walk) <= 64, "room for a walk");
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + L::kBarOff);
   uint64_t* kv_empty = kv_full + L::kSlots;
   uint64_t* q_full = kv_empty + L::kSlots;  // [2] a unit's q tile is in shared memory
@@ -133,13 +166,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   uint64_t* converters = done + 1;          // a barrier of their own
   float2* evals = reinterpret_cast<float2*>(sm + L::kEOff);
   float2* ered = evals + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kEOff + 48);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kEOff + 52);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kEOff + 80);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kEOff + 84);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    p.tails[blockIdx.x] = make_int4(0, 0, 0, 0);
     for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(&kv_full[i], 4);
+      mbar_init(&kv_full[i], kConvert / 32);
       mbar_init(&kv_empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -151,21 +185,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       mbar_init(&e_empty[t], 8);
     }
     mbar_init(done, 1);
-    mbar_init(converters, 4);
+    mbar_init(converters, kConvert / 32);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == kIssue) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
 
   // The line's length, this block's share, and where that begins: tiles of each
   // sequence (a warp each), their sums, then the place in the sequence.
-  Walk w;
-  w.tpt = 128 / p.G;
-  int64_t total, shares;
   {
+    Walk w;
+    w.tpt = 128 / p.G;
+    int64_t total, shares;
     int64_t* line = reinterpret_cast<int64_t*>(sm);  // [B] <= kAttendMaxBatch, before any tile
     for (w.b = warp; w.b < p.B; w.b += kThreads / 32) {
       w.load(p);
@@ -190,16 +224,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
       int b = b0;
       for (; w.pos >= before + line[b]; ++b) before += line[b];
-      misc[13] = b;
-      misc[14] = (w.pos - before) / (line[b] / p.Hkv);
-      misc[15] = (w.pos - before) % (line[b] / p.Hkv);
+      misc[20] = b;
+      misc[21] = (w.pos - before) / (line[b] / p.Hkv);
+      misc[22] = (w.pos - before) % (line[b] / p.Hkv);
     }
     __syncthreads();
     if (w.pos < w.end) {
-      w.b = (int)misc[13];
-      w.h = (int)misc[14];
+      w.b = (int)misc[20];
+      w.h = (int)misc[21];
       w.load(p);
-      int64_t rest = misc[15];
+      int64_t rest = misc[22];
       int found = -1;
       for (int q0 = 0; found < 0; q0 += 32) {  // every warp for itself
         const int n = q0 + lane < w.units() ? w.tiles_of(q0 + lane) : 0;
@@ -222,15 +256,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       w.tile = (int)rest;
       w.tiles = w.tiles_of(found);
     }
+    if (lane == 0 && warp <= kIssue) walks[warp] = w;
+    if (threadIdx.x == 0) {
+      misc[23] = total;
+      misc[24] = shares;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int4 tail = make_int4(0, 0, 0, 0);
+  Walk& w = walks[min(warp, kIssue)];
+  auto advance = [&]() {  // by a whole warp
+    __syncwarp();
+    if (lane == 0) w.next(p);
+    __syncwarp();
+  };
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
+    regs_inc<kRegsSoftmax>();
     const int t = warp >> 2;
     const int rr = (warp & 3) * 32 + lane;  // row of the tile = lane of tensor memory
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -290,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       const float2 e = evals[seg & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&e_empty[seg & 1]);
-      f *= e.x;
+      f = fmaxf(f * e.x, 1.17549435e-38f);  // not zero: a masked score stays at -infinity
 
       float m = -INFINITY, l = 0.f;  // reference maximum, sum of weights
       for (int i = 0; i < mine; ++i, ++it) {
@@ -299,21 +344,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         tc_fence_after();
         const int sees = last - (w.tile + i) * kKeys;  // columns up to this one are seen
         const bool masked = __any_sync(0xffffffffu, sees < kKeys - 1);
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[32];
-          tmem_ld32(st + c * 32, x);
+        // the row goes by twice, 64 scores at a time: held whole it would take the
+        // registers that the conversion needs
+        auto scores = [&](int half, uint32_t (&x)[64]) {
+          tmem_ld32(st + half * 64, *reinterpret_cast<uint32_t(*)[32]>(x));
+          tmem_ld32(st + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
           tmem_wait_ld();
           if (masked) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c * 32 + k <= sees) top = fmaxf(top, __uint_as_float(x[k]));
-          } else {
+            for (int k = 0; k < 64; ++k)
+              if (half * 64 + k > sees) x[k] = __float_as_uint(-INFINITY);
+          }
+        };
+        uint32_t x[64];
+        float top = -INFINITY, top2 = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(x[k]));
+        for (int half = 0; half < 2; ++half) {
+          scores(half, x);
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            top = max3(top, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            top2 = max3(top2, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
           }
         }
+        top = fmaxf(top, top2);
         const float mt = top == -INFINITY ? -INFINITY : top * f;
         const bool grows = mt > m + kSlack || (m == -INFINITY && mt > -INFINITY);
         if (__any_sync(0xffffffffu, grows)) {
@@ -322,37 +376,34 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           l *= a;
           if (i > 0) {  // the product of the tile before is in: its commit comes before s_full's
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t x[32];
-              tmem_ld32(ot + c * 32, x);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t y[16];
+              tmem_ld16(ot + c * 16, y);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * a);
-              tmem_st32(ot + c * 32, x);
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
+              tmem_st16(ot + c * 16, y);
             }
           }
         }
         const float off = kShift - (m == -INFINITY ? 0.f : m);
+        const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[32], y[16];
-          tmem_ld32(st + c * 32, x);
-          tmem_wait_ld();
-          float sum = 0.f;
+        for (int half = 0; half < 2; ++half) {
+          scores(half, x);
+          uint32_t y[32];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float u = exp2_fast(fmaf(__uint_as_float(x[k]), f, off));
-            float v = exp2_fast(fmaf(__uint_as_float(x[k + 1]), f, off));
-            if (masked) {
-              if (c * 32 + k > sees) u = 0.f;
-              if (c * 32 + k + 1 > sees) v = 0.f;
-            }
-            sum += u + v;
-            y[k / 2] = pack2<__half>(u, v);
+          for (int k = 0; k < 32; ++k) {
+            float2 v = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, off2);
+            v.x = exp2_fast(v.x);
+            v.y = exp2_fast(v.y);
+            sum = add2(sum, v);
+            y[k] = pack2<__half>(v.x, v.y);
           }
-          l += sum;
-          tmem_st16(st + c * 16, y);
+          tmem_st32(st + half * 32, y);
         }
+        l += sum.x + sum.y;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -405,39 +456,40 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       } else if (valid) {
         reinterpret_cast<float4*>(part + 256 * D)[t * 128 + rr] = make_float4(m, l, e.y, 0.f);
       }
-      if (begins && !ends) {
+      if (begins && !ends && threadIdx.x == 0) {
         int k = blockIdx.x;
-        while (total * (k + 1) / shares < w.pos + w.tiles) ++k;
-        tail = make_int4(k - (int)blockIdx.x, w.b, w.h, w.qt);
+        while (misc[23] * (k + 1) / misc[24] < w.pos + w.tiles) ++k;
+        p.tails[blockIdx.x] = make_int4(k - (int)blockIdx.x, w.b, w.h, w.qt);
       }
       ++seg;
-      w.next(p);
+      advance();
     }
-    if (threadIdx.x == 0) p.tails[blockIdx.x] = ok ? tail : make_int4(0, 0, 0, 0);
-  } else if (warp < 12) {
+  } else if (warp < kIssue) {
     // ------------------------------------------------------------ codes to f16
-    constexpr int kLoads = kKeys * D / 16 / 128;    // 16-byte pieces of a thread
-    constexpr int kPieces = D / 16;                  // of a row
+    regs_dec<kRegsConvert>();
+    constexpr int kLoads = kKeys * D / 16 / kConvert;  // 16-byte pieces of a thread
+    constexpr int kPieces = D / 16;                    // of a row
     const int cw = warp - 8, ct = threadIdx.x - 256;
     // eight lanes that store together write two rows, so that no bank is met twice
     const int piece = D == 128 ? (lane & 3) + 4 * (lane >> 4) : lane & 3;
     const int sub = D == 128 ? cw * 4 + ((lane >> 2) & 3) : cw * 8 + (lane >> 2);
-    constexpr int kRowsPerLoad = 128 / kPieces;
+    constexpr int kRowsPerLoad = kConvert / kPieces;
     int u = 0, seg = 0, syncs = 0;
     bool ok = true;
     while (w.pos < w.end && ok) {
       const int cnt = w.count(), n = max(w.count(0, cnt), w.count(1, cnt));
       const int* ids = p.table + (int64_t)w.b * p.max_pages;
+      const int first = w.tile * kKeys, kv = w.kv, h = w.h;
       // references: the largest scales of the pages of this share
       float ek = 0.f, ev = 0.f;
       {
-        const int first = w.tile * kKeys, stop = min(w.kv, (w.tile + n) * kKeys);
+        const int stop = min(kv, first + n * kKeys);
         const int pages = stop > first ? ((stop - 1) >> p.page_log2) + 1 : 0;
-        for (int g = (first >> p.page_log2) + ct; g < pages; g += 128) {
+        for (int g = (first >> p.page_log2) + ct; g < pages; g += kConvert) {
           const int id = ids[g];
           if (id >= 0 && id < p.num_pages) {
-            ek = fmaxf(ek, __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + w.h));
-            ev = fmaxf(ev, __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + w.h));
+            ek = fmaxf(ek, __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + h));
+            ev = fmaxf(ev, __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + h));
           } else {
             atomicOr(p.status, kDevBadIndex);
           }
@@ -449,8 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         }
         if (lane == 0) ered[cw] = make_float2(ek, ev);
         if (!(ok = warps_sync(converters, syncs, p.status, abort_flag))) break;
-        ek = fmaxf(fmaxf(ered[0].x, ered[1].x), fmaxf(ered[2].x, ered[3].x));
-        ev = fmaxf(fmaxf(ered[0].y, ered[1].y), fmaxf(ered[2].y, ered[3].y));
+#pragma unroll
+        for (int k = 0; k < kConvert / 32; ++k) {
+          ek = fmaxf(ek, ered[k].x);
+          ev = fmaxf(ev, ered[k].y);
+        }
         if (cw == 0) {  // one warp alone waits: the others may be a unit behind it
           if (seg >= 2)
             ok = warp_wait(&e_empty[seg & 1], ((seg >> 1) - 1) & 1, p.status, abort_flag);
@@ -465,24 +520,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       }
       const float kinv = ek > 0.f ? 1.f / ek : 0.f, vinv = ev > 0.f ? 1.f / ev : 0.f;
 
-      // lane g < 8 knows the page and scales of tokens 16 g .. 16 g + 15 of a tile
-      auto page_of = [&](int i) {
-        const int tok = (w.tile + i) * kKeys + (lane & 7) * 16;
-        const int id = i < n && tok < w.kv ? ids[tok >> p.page_log2] : -1;
-        return id >= 0 && id < p.num_pages ? id : -1;
+      // lane g < 8 knows the page and scales of tokens 16 g .. 16 g + 15 of a tile.
+      // Each is asked for a whole tile before it is used, in loads that stay in
+      // place: a page number at tile i for the codes of tile i + 2, scales at tile i
+      // for the conversion of tile i + 1.
+      auto ask_page = [&](int i) {
+        const int tok = first + i * kKeys + (lane & 7) * 16;
+        return load_word(ids + (tok >> p.page_log2), i < n && tok < kv, -1);
+      };
+      auto known = [&](int id) { return id >= 0 && id < p.num_pages ? id : -1; };
+      auto ask_scale = [&](int id, int which) {
+        return __int_as_float(load_word(
+            reinterpret_cast<const int*>(p.kvscale[which]) + (int64_t)id * p.Hkv + h, id >= 0, 0));
       };
       auto load = [&](uint4 (&x)[kLoads], int i, int id, int which) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
           const int r = j * kRowsPerLoad + sub;
           const int at = __shfl_sync(0xffffffffu, id, r >> 4);
-          const int tok = (w.tile + i) * kKeys + r;
-          x[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (at >= 0 && tok < w.kv)
-            x[j] = __ldg(reinterpret_cast<const uint4*>(
-                p.codes[which] +
-                ((((int64_t)at * p.Hkv + w.h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1))) * D +
-                piece * 16));
+          const int tok = first + i * kKeys + r;
+          x[j] = load_codes(
+              p.codes[which] +
+                  ((((int64_t)at * p.Hkv + h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1))) * D +
+                  piece * 16,
+              at >= 0 && tok < kv);
         }
       };
       auto store = [&](const uint4 (&x)[kLoads], float factor, int slot) {
@@ -507,38 +568,42 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         __syncwarp();
         if (lane == 0) mbar_arrive(&kv_full[slot]);
       };
-      auto scale_of = [&](int id, int which, float inv) {
-        return id >= 0 ? __ldg(p.kvscale[which] + (int64_t)id * p.Hkv + w.h) * inv : 0.f;
-      };
       auto acquire = [&]() {
         return u < L::kSlots ||
                warp_wait(&kv_empty[u % L::kSlots], ((u / L::kSlots) - 1) & 1, p.status, abort_flag);
       };
       uint4 xk[kLoads], xv[kLoads];
-      int id = page_of(0), id_next = page_of(1);
+      int id = known(ask_page(0)), id1 = ask_page(1);
+      float fk = ask_scale(id, 0) * kinv, fv = ask_scale(id, 1) * vinv;
       load(xk, 0, id, 0);
       for (int i = 0; i < n; ++i) {
-        const float fk = scale_of(id, 0, kinv), fv = scale_of(id, 1, vinv);
+        const int id2 = ask_page(i + 2);
+        id1 = known(id1);
+        const float fk1 = ask_scale(id1, 0), fv1 = ask_scale(id1, 1);
         load(xv, i, id, 1);
         if (!(ok = acquire())) break;
         store(xk, fk, u % L::kSlots);
         ++u;
-        id = id_next;
-        id_next = page_of(i + 2);
-        if (i + 1 < n) load(xk, i + 1, id, 0);
+        load(xk, i + 1, id1, 0);
         if (!(ok = acquire())) break;
         store(xv, fv, u % L::kSlots);
         ++u;
+        id = id1;
+        id1 = id2;
+        fk = fk1 * kinv;
+        fv = fv1 * vinv;
       }
       if (!ok) break;
       ++seg;
-      w.next(p);
+      advance();
     }
-  } else if (elect_one()) {
+  } else {
+    regs_dec<kRegsIssue>();
+    if (warp == kIssue && elect_one()) {
     // ------------------------------------------------------------ products
-    int u = 0;                // K and V tiles so far
-    int it[2] = {0, 0};       // score tiles of each row tile so far
-    int units[2] = {0, 0};    // units in which it had any
+    // few registers: parities in bits, row tiles in loops that stay loops
+    int u = 0;                          // K and V tiles so far
+    uint32_t q_parity = 0, p_parity = 0;  // bit t: of the next wait for row tile t
     bool ok = true;
     auto slot = [&](int k) { return base + L::kSlotOff + (uint32_t)(k % L::kSlots) * L::kSlot; };
     auto wait_kv = [&](int k) {
@@ -546,41 +611,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     };
     auto scores = [&](int t, int k) {  // S = Q K^T with the K tile k
       tc_fence_after();
+      const uint32_t q = base + t * L::kQ, kt = slot(k), s = tmem + t * 128;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-        mma_ss(tmem + t * 128, smem_desc_sw128(base + t * L::kQ + off, 16, 1024),
-               smem_desc_sw128(slot(k) + off, 16, 1024), IDESC_QK, kk > 0 ? 1u : 0u);
+        mma_ss(s, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(kt + off, 16, 1024), IDESC_QK,
+               kk > 0 ? 1u : 0u);
       }
       mma_commit(&s_full[t]);
     };
     while (w.pos < w.end && ok) {
-      const int cnt = w.count();
-      const int c[2] = {w.count(0, cnt), w.count(1, cnt)};
-      const int n = max(c[0], c[1]);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (c[t] == 0) continue;
-        ok = mbar_wait(&q_full[t], units[t] & 1, p.status, abort_flag) && wait_kv(u);
+      const int cnt = w.count(), c0 = w.count(0, cnt), c1 = w.count(1, cnt), n = max(c0, c1);
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        if ((t ? c1 : c0) == 0) continue;
+        ok = mbar_wait(&q_full[t], (q_parity >> t) & 1, p.status, abort_flag) && wait_kv(u);
         if (!ok) break;
-        ++units[t];
+        q_parity ^= 1u << t;
         scores(t, u);
       }
       if (ok && n > 0) mma_commit(&kv_empty[u % L::kSlots]);
+#pragma unroll 1
       for (int i = 0; i < n && ok; ++i, u += 2) {
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (i >= c[t]) continue;
-          ok = mbar_wait(&p_full[t], it[t] & 1, p.status, abort_flag) && wait_kv(u + 1);
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          const int c = t ? c1 : c0;
+          if (i >= c) continue;
+          ok = mbar_wait(&p_full[t], (p_parity >> t) & 1, p.status, abort_flag) && wait_kv(u + 1);
           if (!ok) break;
-          ++it[t];
+          p_parity ^= 1u << t;
           tc_fence_after();
+          const uint32_t vt = slot(u + 1), pt = tmem + t * 128;
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)  // O += P V
-            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                   smem_desc_sw128(slot(u + 1) + kk * 2048, kKeys * 128, 1024), IDESC_PV,
-                   i > 0 || kk > 0 ? 1u : 0u);
-          if (i + 1 < c[t]) {
+            mma_ts(pt + 256, pt + kk * 8, smem_desc_sw128(vt + kk * 2048, kKeys * 128, 1024),
+                   IDESC_PV, i > 0 || kk > 0 ? 1u : 0u);
+          if (i + 1 < c) {
             ok = wait_kv(u + 2);
-            if (ok) scores(t, u + 2);
+            if (!ok) break;
+            scores(t, u + 2);
           } else {
             mma_commit(&o_full[t]);
           }
@@ -593,12 +662,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     }
     mma_commit(done);
     mbar_wait_drain(done, 0);
+    }
   }
   __syncwarp();
   griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kIssue) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
