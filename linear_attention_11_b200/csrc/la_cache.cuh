@@ -87,7 +87,8 @@ __device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
 }
 
 // ---------------------------------------------------------------- e4m3
-// Two codes (low byte first) as f16x2, exactly: f16 has e4m3's numbers.
+// The two codes in a word's lower half (low byte first) as f16x2, exactly: f16
+// has e4m3's numbers.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   uint32_t r;
   asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"

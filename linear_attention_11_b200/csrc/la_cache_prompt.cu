@@ -17,7 +17,9 @@
 //                   products read them: pages are gathered by plain 16-byte loads one
 //                   half tile ahead, as the conversion needs the codes in registers
 //                   anyway
-//   warp 16         issues the products (17 to 19 fill up its warpgroup: registers go by those)
+//   warp 16         issues the products
+//   warp 17         goes ahead from unit to unit and writes down for the others what
+//                   they are (18 and 19 fill up the warpgroup: registers go by those)
 // The scale of a page against the largest of the block's share of the unit is a
 // power of two and goes into the conversion (exact in f16 down to 2^-15 of the
 // largest; below, codes lose bits that weigh 2^-24 of it), so one factor a row is
@@ -35,15 +37,27 @@
 namespace la {
 namespace {
 
-constexpr int kKeys = 128;  // tokens of a key tile
+constexpr int kKeys = 128;  // tokens of a key tile: what is converted at a time
 constexpr int kThreads = 640, kConvert = 256;
-constexpr int kIssue = 16;  // the warp that issues the products
+constexpr int kIssue = 16, kPlan = 17;  // the warps that issue products and plan
+constexpr int kPlans = 4;               // units that the plan is ahead at most
 constexpr float kShift = kPromptShift;
 constexpr float kSlack = 8.f;  // growth of a row's maximum that is let pass
 constexpr int kMinTiles = 2;
 // registers of a thread after the split; 640 x 96 at launch
-constexpr int kRegsSoftmax = 136, kRegsConvert = 80, kRegsIssue = 40;
+constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 56;
 static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= 640 * 96, "registers");
+
+// A block's part of a unit, as the planning warp writes it down.
+struct Unit {
+  int b, h, qt;
+  int tile, n;       // first key tile and how many; n < 0: no more units
+  int c[2];          // how many score tiles of those each row tile sees
+  int kv, nq;
+  int begins, ends;  // whether the unit's first and last tiles are among them
+  int follow;        // of a unit that begins but does not end: blocks that hold the rest
+  float ek, ev;      // largest scales of the pages
+};
 
 template <int D>
 struct PromptLayout {
@@ -52,12 +66,10 @@ struct PromptLayout {
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kSlotOff = 2 * kQ;
   static constexpr int kMiscOff = kSlotOff + kSlots * kSlot;
-  // scan scratch 20 x 8, start 3 x 8, line and shares 2 x 8 | walks | barriers | e values
-  static constexpr int kBars = 2 * kSlots + 2 * 6 + 2;
-  static constexpr int kWalkOff = kMiscOff + 208;
-  static constexpr int kBarOff = kWalkOff + 17 * 64;
-  static constexpr int kEOff = kBarOff + kBars * 8;  // float2 e[2], float2 red[8]
-  static constexpr int kEnd = kEOff + 80 + 16;       // tmem slot, abort flag
+  static constexpr int kUnitOff = kMiscOff + 23 * 8;  // scan scratch 20 x 8, start 3 x 8
+  static constexpr int kBarOff = kUnitOff + kPlans * 64;
+  static constexpr int kBars = 2 * kSlots + 2 * 4 + 2 * kPlans + 1;
+  static constexpr int kEnd = kBarOff + kBars * 8 + 16;  // tmem slot, abort flag
   static constexpr int kBytes = kEnd + 1024;
 };
 
@@ -66,9 +78,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
          ((uint32_t)(M >> 4) << 24);
 }
 
-// A block's walk along its share of the line of key tiles: units (b, h, qt).  Each
-// warp has one in shared memory, which its lane 0 moves on: in registers it would
-// crowd out the score rows.
+// A block's walk along its share of the line of key tiles: units (b, h, qt).
 struct Walk {
   int64_t pos, end;
   int b, h, qt;
@@ -83,16 +93,18 @@ struct Walk {
     nq = ok ? (int)n : 0;
   }
   __device__ int units() const { return (nq + 2 * tpt - 1) / (2 * tpt); }
-  // key tiles that row tile t of unit q sees (0: none, or no such rows)
+  // score tiles that row tile t of unit q sees (0: none, or no such rows)
   __device__ int sees(int q, int t) const {
     const int first = (q * 2 + t) * tpt;
     if (first >= nq) return 0;
     const int n = kv - nq + min(nq, first + tpt);
     return n > 0 ? (n + kKeys - 1) / kKeys : 0;
   }
-  __device__ int tiles_of(int q) const { return max(1, max(sees(q, 0), sees(q, 1))); }
+  __device__ int tiles_of(int q) const {
+    return max(1, max(sees(q, 0), sees(q, 1)));
+  }
   __device__ int count() const { return (int)min((int64_t)(tiles - tile), end - pos); }
-  // the tiles of row tile t in this share of the unit
+  // the score tiles of row tile t in this share's n key tiles of the unit
   __device__ int count(int t, int n) const { return max(0, min(n, sees(qt, t) - tile)); }
   __device__ void next(const AttendParams& p) {
     pos += tiles - tile;
@@ -149,25 +161,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
   int64_t* misc = reinterpret_cast<int64_t*>(sm + L::kMiscOff);
-  Walk* walks = reinterpret_cast<Walk*>(sm + L::kWalkOff);
-  static_assert(sizeof(Walk) <= 64, "room for a walk");
+  auto unit_at = [&](int seg) -> Unit& {
+    return *reinterpret_cast<Unit*>(sm + L::kUnitOff + (seg % kPlans) * 64);
+  };
+  static_assert(sizeof(Unit) <= 64, "room for a unit");
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + L::kBarOff);
   uint64_t* kv_empty = kv_full + L::kSlots;
   uint64_t* q_full = kv_empty + L::kSlots;  // [2] a unit's q tile is in shared memory
   uint64_t* s_full = q_full + 2;            // [2] a score tile is computed
   uint64_t* p_full = s_full + 2;            // [2] its weights are written, O is rescaled
   uint64_t* o_full = p_full + 2;            // [2] a unit's last product with V is added
-  // [2], units in turn: a unit's scale references are known; every softmax warp has
-  // read them.  One barrier for all units would not do: the copies may be two units
-  // ahead, and a wait cannot tell a phase from the one two after it
-  uint64_t* e_full = o_full + 2;
-  uint64_t* e_empty = e_full + 2;
-  uint64_t* done = e_empty + 2;
-  uint64_t* converters = done + 1;          // a barrier of their own
-  float2* evals = reinterpret_cast<float2*>(sm + L::kEOff);
-  float2* ered = evals + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kEOff + 80);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kEOff + 84);
+  uint64_t* u_full = o_full + 2;            // [kPlans] a unit is written down
+  uint64_t* u_empty = u_full + kPlans;      // [kPlans] every role has read it
+  uint64_t* done = u_empty + kPlans;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -181,11 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_full[t], 1);
-      mbar_init(&e_full[t], 1);
-      mbar_init(&e_empty[t], 8);
+    }
+    for (int k = 0; k < kPlans; ++k) {
+      mbar_init(&u_full[k], 1);
+      mbar_init(&u_empty[k], 8 + kConvert / 32 + 1);
     }
     mbar_init(done, 1);
-    mbar_init(converters, kConvert / 32);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -196,10 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
 
   // The line's length, this block's share, and where that begins: tiles of each
   // sequence (a warp each), their sums, then the place in the sequence.
+  const int tpt = 128 / p.G;
+  Walk w;
+  w.tpt = tpt;
+  int64_t total, shares;
   {
-    Walk w;
-    w.tpt = 128 / p.G;
-    int64_t total, shares;
     int64_t* line = reinterpret_cast<int64_t*>(sm);  // [B] <= kAttendMaxBatch, before any tile
     for (w.b = warp; w.b < p.B; w.b += kThreads / 32) {
       w.load(p);
@@ -229,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       misc[22] = (w.pos - before) % (line[b] / p.Hkv);
     }
     __syncthreads();
-    if (w.pos < w.end) {
+    if (warp == kPlan && w.pos < w.end) {
       w.b = (int)misc[20];
       w.h = (int)misc[21];
       w.load(p);
       int64_t rest = misc[22];
       int found = -1;
-      for (int q0 = 0; found < 0; q0 += 32) {  // every warp for itself
+      for (int q0 = 0; found < 0; q0 += 32) {
         const int n = q0 + lane < w.units() ? w.tiles_of(q0 + lane) : 0;
         int in = n;
 #pragma unroll
@@ -256,22 +266,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       w.tile = (int)rest;
       w.tiles = w.tiles_of(found);
     }
-    if (lane == 0 && warp <= kIssue) walks[warp] = w;
-    if (threadIdx.x == 0) {
-      misc[23] = total;
-      misc[24] = shares;
-    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk& w = walks[min(warp, kIssue)];
-  auto advance = [&]() {  // by a whole warp
-    __syncwarp();
-    if (lane == 0) w.next(p);
-    __syncwarp();
+  // by a whole warp: unit `seg` once it is written down, and that it has been read
+  auto wait_unit = [&](int seg) {
+    return warp_wait_brief(&u_full[seg % kPlans], (seg / kPlans) & 1, abort_flag);
   };
+  auto release_unit = [&](int seg) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&u_empty[seg % kPlans]);
+  };
+  bool ok = true;
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -282,31 +290,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     const uint32_t st = tmem + lanes + t * 128, ot = tmem + lanes + 256 + t * 128;
     const uint32_t sq = base + t * L::kQ;
     int it = 0;    // score tiles so far
-    int seg = 0;   // units so far
     int used = 0;  // units in which this row tile had any
-    bool ok = true;
-    while (w.pos < w.end && ok) {
-      const int n = w.count(), mine = w.count(t, n);
-      const int token = (w.qt * 2 + t) * w.tpt + rr / p.G, head = w.h * p.G + rr % p.G;
-      const bool valid = rr < w.tpt * p.G && token < w.nq;
-      const int64_t row = ((int64_t)w.b * p.Hq + head) * p.N + token;
-      const int last = valid ? w.kv - w.nq + token : 0x7fffffff;  // last key that the row sees
+    for (int seg = 0;; ++seg) {
+      if (!(ok = wait_unit(seg))) break;
+      const Unit& unit = unit_at(seg);
+      const int mine = unit.c[t], first = unit.tile * kKeys, b = unit.b, h = unit.h, qt = unit.qt;
+      if (unit.n < 0) break;
+      const bool begins = unit.begins, whole = begins && unit.ends;
+      const float ek = unit.ek, ev = unit.ev;
+      const int token = (qt * 2 + t) * tpt + rr / p.G;
+      const bool valid = rr < tpt * p.G && token < unit.nq;
+      const int64_t row = ((int64_t)b * p.Hq + h * p.G + rr % p.G) * p.N + token;
+      const int last = valid ? unit.kv - unit.nq + token : 0x7fffffff;  // last key that the row sees
+      if (threadIdx.x == 0 && unit.follow > 0)
+        p.tails[blockIdx.x] = make_int4(unit.follow, b, h, qt);
+      release_unit(seg);
       float f = 0.f;
       if (mine > 0) {
         // q: largest entry of the row into [2^14, 2^15), then f16; the sign of the
         // scale goes here too, so that the scores' factor is not negative
-        uint4 x[D / 8];
+        // (read twice, the second time from a cache: a whole row would fill the registers)
         float top = 0.f;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + row * D);
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) x[j] = valid ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
+#pragma unroll 4
         for (int j = 0; j < D / 8; ++j) {
-          const uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+          const uint4 x = valid ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 v = unpack2<T>(u[k]);
-            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+            top = max3(top, fabsf(v.x), fabsf(v.y));
           }
         }
         const int ex = (int)(__float_as_uint(top) >> 23) - 127;
@@ -314,9 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         const float up = scaled ? pow2i(max(min(14 - ex, 127), -126)) : 1.f;
         f = fabsf(p.scale) * kLog2e / up;
         const float q1 = p.scale < 0.f ? -up : up;
-#pragma unroll
+#pragma unroll 4
         for (int j = 0; j < D / 8; ++j) {
-          const uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+          const uint4 x = valid ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
           uint32_t v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -330,22 +344,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
       }
-      ok = warp_wait(&e_full[seg & 1], (seg >> 1) & 1, p.status, abort_flag);
-      if (!ok) break;
-      const float2 e = evals[seg & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&e_empty[seg & 1]);
-      f = fmaxf(f * e.x, 1.17549435e-38f);  // not zero: a masked score stays at -infinity
+      f = fmaxf(f * ek, 1.17549435e-38f);  // not zero: a masked score stays at -infinity
 
       float m = -INFINITY, l = 0.f;  // reference maximum, sum of weights
       for (int i = 0; i < mine; ++i, ++it) {
-        ok = warp_wait(&s_full[t], it & 1, p.status, abort_flag);
+        ok = warp_wait_brief(&s_full[t], it & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const int sees = last - (w.tile + i) * kKeys;  // columns up to this one are seen
+        const int sees = last - first - i * kKeys;  // columns up to this one are seen
         const bool masked = __any_sync(0xffffffffu, sees < kKeys - 1);
-        // the row goes by twice, 64 scores at a time: held whole it would take the
-        // registers that the conversion needs
+        // The row goes by twice, 64 scores at a time: held whole it would take the
+        // registers that the conversion needs.
         auto scores = [&](int half, uint32_t (&x)[64]) {
           tmem_ld32(st + half * 64, *reinterpret_cast<uint32_t(*)[32]>(x));
           tmem_ld32(st + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
@@ -357,53 +366,54 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           }
         };
         uint32_t x[64];
-        float top = -INFINITY, top2 = -INFINITY;
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           scores(half, x);
 #pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            top = max3(top, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-            top2 = max3(top2, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
-          }
+          for (int k = 0; k < 64; k += 2)
+            top[(k >> 1) & 3] = max3(top[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
         }
-        top = fmaxf(top, top2);
-        const float mt = top == -INFINITY ? -INFINITY : top * f;
+        top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        const float mt = top[0] == -INFINITY ? -INFINITY : top[0] * f;
         const bool grows = mt > m + kSlack || (m == -INFINITY && mt > -INFINITY);
         if (__any_sync(0xffffffffu, grows)) {
+          // a new reference: the sum so far and O go by 2^(old - new)
           const float a = grows ? exp2_fast(m - mt) : 1.f;
           if (grows) m = mt;
           l *= a;
-          if (i > 0) {  // the product of the tile before is in: its commit comes before s_full's
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
+          if (i > 0) {  // the product of the tile before is in: it was issued before these scores
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
               uint32_t y[16];
-              tmem_ld16(ot + c * 16, y);
+              tmem_ld16(ot + k * 16, y);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
-              tmem_st16(ot + c * 16, y);
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a);
+              tmem_st16(ot + k * 16, y);
             }
           }
         }
         const float off = kShift - (m == -INFINITY ? 0.f : m);
         const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-        float2 sum = make_float2(0.f, 0.f);
+        float2 sum = make_float2(l, 0.f), sum2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           scores(half, x);
           uint32_t y[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            float2 v = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, off2);
-            v.x = exp2_fast(v.x);
-            v.y = exp2_fast(v.y);
-            sum = add2(sum, v);
-            y[k] = pack2<__half>(v.x, v.y);
+            float2 w = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, off2);
+            w.x = exp2_fast(w.x);
+            w.y = exp2_fast(w.y);
+            if (k & 1) sum2 = add2(sum2, w);
+            else sum = add2(sum, w);
+            y[k] = pack2<__half>(w.x, w.y);
           }
           tmem_st32(st + half * 32, y);
         }
-        l += sum.x + sum.y;
+        sum = add2(sum, sum2);
+        l = sum.x + sum.y;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -412,11 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       if (!ok) break;
 
       // the unit's output, or its part
-      const bool begins = w.tile == 0, ends = w.tile + n == w.tiles;
       if (mine > 0) {
-        ok = warp_wait(&o_full[t], used & 1, p.status, abort_flag);
-        if (!ok) break;
+        ok = warp_wait_brief(&o_full[t], used & 1, abort_flag);
         ++used;
+        if (!ok) break;
         tc_fence_after();
       }
       float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * 256 * (D + kPartStats);
@@ -432,15 +441,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           for (int k = 0; k < 32; ++k) x[k] = 0u;
         }
         if (!valid) continue;
-        if (begins && ends) {
+        if (whole) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * D + c * 32);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t y[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              y[j] = pack2<T>(__uint_as_float(x[k * 8 + 2 * j]) * inv * e.y,
-                              __uint_as_float(x[k * 8 + 2 * j + 1]) * inv * e.y);
+              y[j] = pack2<T>(__uint_as_float(x[k * 8 + 2 * j]) * inv * ev,
+                              __uint_as_float(x[k * 8 + 2 * j + 1]) * inv * ev);
             dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         } else {
@@ -451,75 +460,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         }
       }
       tc_fence_before();
-      if (valid && begins && ends) {
+      if (valid && whole) {
         if (p.lse) p.lse[row] = (m - kShift + log2f(l)) * kLn2;
       } else if (valid) {
-        reinterpret_cast<float4*>(part + 256 * D)[t * 128 + rr] = make_float4(m, l, e.y, 0.f);
+        reinterpret_cast<float4*>(part + 256 * D)[t * 128 + rr] = make_float4(m, l, ev, 0.f);
       }
-      if (begins && !ends && threadIdx.x == 0) {
-        int k = blockIdx.x;
-        while (misc[23] * (k + 1) / misc[24] < w.pos + w.tiles) ++k;
-        p.tails[blockIdx.x] = make_int4(k - (int)blockIdx.x, w.b, w.h, w.qt);
-      }
-      ++seg;
-      advance();
     }
   } else if (warp < kIssue) {
     // ------------------------------------------------------------ codes to f16
     regs_dec<kRegsConvert>();
     constexpr int kLoads = kKeys * D / 16 / kConvert;  // 16-byte pieces of a thread
     constexpr int kPieces = D / 16;                    // of a row
-    const int cw = warp - 8, ct = threadIdx.x - 256;
+    const int cw = warp - 8;
     // eight lanes that store together write two rows, so that no bank is met twice
     const int piece = D == 128 ? (lane & 3) + 4 * (lane >> 4) : lane & 3;
     const int sub = D == 128 ? cw * 4 + ((lane >> 2) & 3) : cw * 8 + (lane >> 2);
     constexpr int kRowsPerLoad = kConvert / kPieces;
-    int u = 0, seg = 0, syncs = 0;
-    bool ok = true;
-    while (w.pos < w.end && ok) {
-      const int cnt = w.count(), n = max(w.count(0, cnt), w.count(1, cnt));
-      const int* ids = p.table + (int64_t)w.b * p.max_pages;
-      const int first = w.tile * kKeys, kv = w.kv, h = w.h;
-      // references: the largest scales of the pages of this share
-      float ek = 0.f, ev = 0.f;
-      {
-        const int stop = min(kv, first + n * kKeys);
-        const int pages = stop > first ? ((stop - 1) >> p.page_log2) + 1 : 0;
-        for (int g = (first >> p.page_log2) + ct; g < pages; g += kConvert) {
-          const int id = ids[g];
-          if (id >= 0 && id < p.num_pages) {
-            ek = fmaxf(ek, __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + h));
-            ev = fmaxf(ev, __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + h));
-          } else {
-            atomicOr(p.status, kDevBadIndex);
-          }
-        }
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) {
-          ek = fmaxf(ek, __shfl_xor_sync(0xffffffffu, ek, k));
-          ev = fmaxf(ev, __shfl_xor_sync(0xffffffffu, ev, k));
-        }
-        if (lane == 0) ered[cw] = make_float2(ek, ev);
-        if (!(ok = warps_sync(converters, syncs, p.status, abort_flag))) break;
-#pragma unroll
-        for (int k = 0; k < kConvert / 32; ++k) {
-          ek = fmaxf(ek, ered[k].x);
-          ev = fmaxf(ev, ered[k].y);
-        }
-        if (cw == 0) {  // one warp alone waits: the others may be a unit behind it
-          if (seg >= 2)
-            ok = warp_wait(&e_empty[seg & 1], ((seg >> 1) - 1) & 1, p.status, abort_flag);
-          if (!ok) break;
-          if (lane == 0) {
-            evals[seg & 1] = make_float2(ek, ev);
-            mbar_arrive(&e_full[seg & 1]);
-          }
-        }
-        // ered may be written again
-        if (!(ok = warps_sync(converters, syncs, p.status, abort_flag))) break;
-      }
-      const float kinv = ek > 0.f ? 1.f / ek : 0.f, vinv = ev > 0.f ? 1.f / ev : 0.f;
-
+    // place of this thread's first eight codes in a slot; the next eight are beside
+    // them, which the swizzle keeps at an address that differs in bit 4 alone
+    const uint32_t store_at = (piece >> 2) * (kKeys * 128) + sub * 128 +
+                              ((((piece & 3) * 2) ^ (sub & 7)) << 4);
+    int u = 0;
+    for (int seg = 0;; ++seg) {
+      if (!(ok = wait_unit(seg))) break;
+      const Unit& unit = unit_at(seg);
+      const int n = max(unit.c[0], unit.c[1]), first = unit.tile * kKeys, kv = unit.kv, h = unit.h;
+      if (unit.n < 0) break;
+      const int* ids = p.table + (int64_t)unit.b * p.max_pages;
+      const float kinv = unit.ek > 0.f ? 1.f / unit.ek : 0.f;
+      const float vinv = unit.ev > 0.f ? 1.f / unit.ev : 0.f;
+      release_unit(seg);
       // lane g < 8 knows the page and scales of tokens 16 g .. 16 g + 15 of a tile.
       // Each is asked for a whole tile before it is used, in loads that stay in
       // place: a page number at tile i for the codes of tile i + 2, scales at tile i
@@ -533,36 +503,40 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         return __int_as_float(load_word(
             reinterpret_cast<const int*>(p.kvscale[which]) + (int64_t)id * p.Hkv + h, id >= 0, 0));
       };
-      auto load = [&](uint4 (&x)[kLoads], int i, int id, int which) {
+      // A tile's loads: `row` is the first row of codes of the lane's 16 tokens
+      // (-1: none there).
+      auto row_of = [&](int id) {
+        return id >= 0 ? (int)((((int64_t)id * p.Hkv + h) << p.page_log2) +
+                               (((lane & 7) * 16) & ((1 << p.page_log2) - 1)))
+                       : -1;
+      };
+      auto load = [&](uint4 (&x)[kLoads], int i, int row, int which) {
+        const uint8_t* codes = p.codes[which] + piece * 16;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
           const int r = j * kRowsPerLoad + sub;
-          const int at = __shfl_sync(0xffffffffu, id, r >> 4);
-          const int tok = first + i * kKeys + r;
-          x[j] = load_codes(
-              p.codes[which] +
-                  ((((int64_t)at * p.Hkv + h) << p.page_log2) + (tok & ((1 << p.page_log2) - 1))) * D +
-                  piece * 16,
-              at >= 0 && tok < kv);
+          const int at = __shfl_sync(0xffffffffu, row, r >> 4);
+          x[j] = load_codes(codes + (int64_t)(at + (r & 15)) * D,
+                            at >= 0 && first + i * kKeys + r < kv);
         }
       };
       auto store = [&](const uint4 (&x)[kLoads], float factor, int slot) {
-        const uint32_t dst = base + L::kSlotOff + slot * L::kSlot;
+        const uint32_t dst = base + L::kSlotOff + slot * L::kSlot + store_at;
+        const __half2 fh = __float2half2_rn(factor);
+        const uint32_t fw = *reinterpret_cast<const uint32_t*>(&fh);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-          const int r = j * kRowsPerLoad + sub;
-          const __half2 f2 = __float2half2_rn(__shfl_sync(0xffffffffu, factor, r >> 4));
+          const uint32_t fj = __shfl_sync(0xffffffffu, fw, (j * kRowsPerLoad + sub) >> 4);
+          const __half2 f2 = *reinterpret_cast<const __half2*>(&fj);
           const uint32_t c[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
           uint32_t y[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            y[2 * k] = hmul2(e4m3x2_to_f16x2(c[k] & 0xffffu), f2);
+            y[2 * k] = hmul2(e4m3x2_to_f16x2(c[k]), f2);
             y[2 * k + 1] = hmul2(e4m3x2_to_f16x2(c[k] >> 16), f2);
           }
-          const uint32_t at = dst + (piece >> 2) * (kKeys * 128) + r * 128;
-          const int ch = (piece & 3) * 2;
-          st_shared_v4(at + ((ch ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-          st_shared_v4(at + (((ch + 1) ^ (r & 7)) << 4), y[4], y[5], y[6], y[7]);
+          st_shared_v4(dst + j * (kRowsPerLoad * 128), y[0], y[1], y[2], y[3]);
+          st_shared_v4((dst ^ 16) + j * (kRowsPerLoad * 128), y[4], y[5], y[6], y[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -570,48 +544,43 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       };
       auto acquire = [&]() {
         return u < L::kSlots ||
-               warp_wait(&kv_empty[u % L::kSlots], ((u / L::kSlots) - 1) & 1, p.status, abort_flag);
+               warp_wait_brief(&kv_empty[u % L::kSlots], ((u / L::kSlots) - 1) & 1, abort_flag);
       };
       uint4 xk[kLoads], xv[kLoads];
-      int id = known(ask_page(0)), id1 = ask_page(1);
+      int id = known(ask_page(0)), id1 = ask_page(1), row = row_of(id);
       float fk = ask_scale(id, 0) * kinv, fv = ask_scale(id, 1) * vinv;
-      load(xk, 0, id, 0);
+      load(xk, 0, row, 0);
       for (int i = 0; i < n; ++i) {
         const int id2 = ask_page(i + 2);
         id1 = known(id1);
         const float fk1 = ask_scale(id1, 0), fv1 = ask_scale(id1, 1);
-        load(xv, i, id, 1);
+        load(xv, i, row, 1);
         if (!(ok = acquire())) break;
         store(xk, fk, u % L::kSlots);
         ++u;
-        load(xk, i + 1, id1, 0);
+        row = row_of(id1);
+        load(xk, i + 1, row, 0);
         if (!(ok = acquire())) break;
         store(xv, fv, u % L::kSlots);
         ++u;
-        id = id1;
         id1 = id2;
         fk = fk1 * kinv;
         fv = fv1 * vinv;
       }
       if (!ok) break;
-      ++seg;
-      advance();
     }
   } else {
     regs_dec<kRegsIssue>();
     if (warp == kIssue && elect_one()) {
     // ------------------------------------------------------------ products
-    // few registers: parities in bits, row tiles in loops that stay loops
-    int u = 0;                          // K and V tiles so far
-    uint32_t q_parity = 0, p_parity = 0;  // bit t: of the next wait for row tile t
-    bool ok = true;
-    auto slot = [&](int k) { return base + L::kSlotOff + (uint32_t)(k % L::kSlots) * L::kSlot; };
-    auto wait_kv = [&](int k) {
-      return mbar_wait(&kv_full[k % L::kSlots], (k / L::kSlots) & 1, p.status, abort_flag);
-    };
-    auto scores = [&](int t, int k) {  // S = Q K^T with the K tile k
-      tc_fence_after();
-      const uint32_t q = base + t * L::kQ, kt = slot(k), s = tmem + t * 128;
+    // This thread's own instructions are on the path from weights to the next
+    // scores, so there are few: slots and phases are counted, not divided out.
+    int us = 0, up = 0;                     // slot and parity of the next K or V tile
+    uint32_t p_parity = 0, q_parity = 0;    // bit t: of the next wait for row tile t
+    auto slot = [&](int k) { return base + L::kSlotOff + (uint32_t)k * L::kSlot; };
+    auto wait_kv = [&](int k, int par) { return mbar_wait_brief(&kv_full[k], par, abort_flag); };
+    auto scores = [&](int t, uint32_t kt) {  // S = Q K^T
+      const uint32_t q = base + t * L::kQ, s = tmem + t * 128;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
@@ -620,50 +589,130 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       }
       mma_commit(&s_full[t]);
     };
-    while (w.pos < w.end && ok) {
-      const int cnt = w.count(), c0 = w.count(0, cnt), c1 = w.count(1, cnt), n = max(c0, c1);
+    auto next = [&]() {
+      if (++us == L::kSlots) {
+        us = 0;
+        up ^= 1;
+      }
+    };
+    for (int seg = 0; ok; ++seg) {
+      if (!(ok = mbar_wait_brief(&u_full[seg % kPlans], (seg / kPlans) & 1, abort_flag))) break;
+      const Unit& unit = unit_at(seg);
+      if (unit.n < 0) break;
+      const int c0 = unit.c[0], c1 = unit.c[1], n = max(c0, c1);
+      mbar_arrive(&u_empty[seg % kPlans]);
+      if (n == 0) continue;
+      if (!(ok = wait_kv(us, up))) break;
 #pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < 2 && ok; ++t) {
         if ((t ? c1 : c0) == 0) continue;
-        ok = mbar_wait(&q_full[t], (q_parity >> t) & 1, p.status, abort_flag) && wait_kv(u);
+        ok = mbar_wait_brief(&q_full[t], (q_parity >> t) & 1, abort_flag);
         if (!ok) break;
         q_parity ^= 1u << t;
-        scores(t, u);
+        tc_fence_after();
+        scores(t, slot(us));
       }
-      if (ok && n > 0) mma_commit(&kv_empty[u % L::kSlots]);
+      if (!ok) break;
+      mma_commit(&kv_empty[us]);
+      next();
 #pragma unroll 1
-      for (int i = 0; i < n && ok; ++i, u += 2) {
+      for (int i = 0; i < n; ++i) {
+        const int vs = us;
+        if (!(ok = wait_kv(vs, up))) break;
+        next();
+        if (i + 1 < n && !(ok = wait_kv(us, up))) break;
+        const uint32_t vt = slot(vs), kt = slot(us);
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           const int c = t ? c1 : c0;
           if (i >= c) continue;
-          ok = mbar_wait(&p_full[t], (p_parity >> t) & 1, p.status, abort_flag) && wait_kv(u + 1);
+          ok = mbar_wait_brief(&p_full[t], (p_parity >> t) & 1, abort_flag);
           if (!ok) break;
           p_parity ^= 1u << t;
           tc_fence_after();
-          const uint32_t vt = slot(u + 1), pt = tmem + t * 128;
+          const uint32_t pt = tmem + t * 128;
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)  // O += P V
             mma_ts(pt + 256, pt + kk * 8, smem_desc_sw128(vt + kk * 2048, kKeys * 128, 1024),
                    IDESC_PV, i > 0 || kk > 0 ? 1u : 0u);
-          if (i + 1 < c) {
-            ok = wait_kv(u + 2);
-            if (!ok) break;
-            scores(t, u + 2);
-          } else {
-            mma_commit(&o_full[t]);
-          }
+          if (i + 1 < c) scores(t, kt);
+          else mma_commit(&o_full[t]);
         }
         if (!ok) break;
-        mma_commit(&kv_empty[(u + 1) % L::kSlots]);
-        if (i + 1 < n) mma_commit(&kv_empty[(u + 2) % L::kSlots]);
+        mma_commit(&kv_empty[vs]);
+        if (i + 1 < n) {
+          mma_commit(&kv_empty[us]);
+          next();
+        }
       }
-      if (ok) w.next(p);
     }
     mma_commit(done);
     mbar_wait_drain(done, 0);
+    } else if (warp == kPlan) {
+      // ---------------------------------------------------------- plan
+      for (int seg = 0;; ++seg) {
+        if (seg >= kPlans)
+          ok = warp_wait_brief(&u_empty[seg % kPlans], ((seg / kPlans) - 1) & 1, abort_flag);
+        if (!ok) break;
+        Unit& unit = unit_at(seg);
+        const bool more = w.pos < w.end;
+        float ek = 0.f, ev = 0.f;
+        if (more) {
+          // the largest scales among the pages of these tiles
+          const int n = w.count(), c = max(w.count(0, n), w.count(1, n));
+          const int stop = min(w.kv, (w.tile + c) * kKeys);
+          const int g1 = stop > w.tile * kKeys ? ((stop - 1) >> p.page_log2) + 1 : 0;
+          const int* ids = p.table + (int64_t)w.b * p.max_pages;
+#pragma unroll 4
+          for (int g = ((w.tile * kKeys) >> p.page_log2) + lane; g < g1; g += 32) {
+            const int id = __ldg(ids + g);
+            if (id >= 0 && id < p.num_pages) {
+              ek = fmaxf(ek, __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + w.h));
+              ev = fmaxf(ev, __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + w.h));
+            } else {
+              atomicOr(p.status, kDevBadIndex);
+            }
+          }
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) {
+            ek = fmaxf(ek, __shfl_xor_sync(0xffffffffu, ek, k));
+            ev = fmaxf(ev, __shfl_xor_sync(0xffffffffu, ev, k));
+          }
+        }
+        if (lane == 0) {
+          unit.n = -1;
+          if (more) {
+            const int n = w.count();
+            unit.b = w.b;
+            unit.h = w.h;
+            unit.qt = w.qt;
+            unit.tile = w.tile;
+            unit.n = n;
+            unit.c[0] = w.count(0, n);
+            unit.c[1] = w.count(1, n);
+            unit.kv = w.kv;
+            unit.nq = w.nq;
+            unit.begins = w.tile == 0;
+            unit.ends = w.tile + n == w.tiles;
+            unit.follow = 0;
+            if (unit.begins && !unit.ends) {
+              // the share of block k ends at total (k + 1) / shares
+              int k = blockIdx.x;
+              while (total * (k + 1) / shares < w.pos + w.tiles) ++k;
+              unit.follow = k - (int)blockIdx.x;
+            }
+            unit.ek = ek;
+            unit.ev = ev;
+          }
+          mbar_arrive(&u_full[seg % kPlans]);
+        }
+        __syncwarp();
+        if (!more) break;
+        w.next(p);
+      }
     }
   }
+  if (!ok) give_up(p.status, abort_flag);
   __syncwarp();
   griddep_launch_dependents();
   tc_fence_before();

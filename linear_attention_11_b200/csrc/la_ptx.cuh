@@ -91,6 +91,41 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   }
 }
 
+// A wait of few instructions, for kernels whose many waits should not crowd the
+// instruction cache: at most kWaitTries tries, each suspended by the hardware for
+// about 2 us at most (2 s together).  False when they run out or *abort is set;
+// the caller's role then ends with give_up().
+constexpr uint32_t kWaitTries = 1u << 20;
+
+__device__ __forceinline__ bool mbar_wait_brief(uint64_t* bar, uint32_t parity,
+                                                volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (uint32_t n = 0; n < kWaitTries; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(2000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
+
+__device__ __forceinline__ bool warp_wait_brief(uint64_t* bar, uint32_t parity,
+                                                volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_brief(bar, parity, abort) ? 1 : 0) != 0;
+}
+
+__device__ __forceinline__ void give_up(unsigned* status, volatile int* abort) {
+  atomicOr(status, kDevTimeout);
+  *abort = 1;
+}
+
 // mbar_wait by every lane of a warp, with one outcome for the whole warp, so
 // that the warp-collective tcgen05.ld / tcgen05.st that follow run on all
 // lanes or on none.
