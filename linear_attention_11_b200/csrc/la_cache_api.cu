@@ -132,9 +132,10 @@ LA_EXPORT la_status la_cache_read(const la_cache* cache, const int32_t* table,
   if (st == LA_OK) st = check_kv(cache, k, v, dtype, start, count, B, N, true);
   if (st != LA_OK) return st;
   unsigned* status = device_status_ptr();
-  if (!status) return LA_ERR_CUDA;
+  const int sms = device_sms();
+  if (!status || sms <= 0) return LA_ERR_CUDA;
   return from_cuda(launch_cache_read(*cache, table, start, count, k, v, dtype, B, N, max_pages,
-                                     status, static_cast<cudaStream_t>(stream)));
+                                     status, sms, static_cast<cudaStream_t>(stream)));
 }
 
 LA_EXPORT size_t la_cache_attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d) {

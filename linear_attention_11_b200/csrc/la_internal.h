@@ -144,7 +144,8 @@ cudaError_t launch_cache_write(const void* k, const void* v, la_dtype dtype, con
                                cudaStream_t stream);
 cudaError_t launch_cache_read(const la_cache& c, const int32_t* table, const int32_t* start,
                               const int32_t* count, void* k, void* v, la_dtype dtype, int B,
-                              int64_t N, int max_pages, unsigned* status, cudaStream_t stream);
+                              int64_t N, int max_pages, unsigned* status, int sms,
+                              cudaStream_t stream);
 size_t attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d, int sms);
 cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype,
                                 const int32_t* table, const int32_t* kv_len, const int32_t* q_len,
