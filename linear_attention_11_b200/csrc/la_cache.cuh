@@ -169,7 +169,6 @@ constexpr int kPartStats = 4;
 // tile_tokens * G of a tile in use: row r of a tile is head r % G of token r / G.
 struct JoinGeometry {
   int rows, blocks, tile_rows, tile_tokens;
-  float shift;  // weights are 2^shift at the maximum
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -178,8 +177,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Weights are held as 2^shift at a row's reference maximum.
-constexpr float kTokenShift = 15.f, kPromptShift = 7.f;
+// Weights are held as 2^kAttendShift at a row's reference maximum.
+constexpr float kAttendShift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

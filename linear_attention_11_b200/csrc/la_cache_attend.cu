@@ -43,8 +43,8 @@ cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype
                             ? launch_cache_token(p, c, dtype, (int)N * p.G, s.ctas, stream)
                             : launch_cache_prompt(p, dtype, c.d, s.ctas, stream);
   if (e != cudaSuccess) return e;
-  const JoinGeometry g = s.token ? JoinGeometry{s.rows, 1, s.rows, (int)N, kTokenShift}
-                                 : JoinGeometry{256, 2, 128, 128 / p.G, kPromptShift};
+  const JoinGeometry g = s.token ? JoinGeometry{s.rows, 1, s.rows, (int)N}
+                                 : JoinGeometry{256, 2, 128, 128 / p.G};
   return launch_cache_join(p, g, dtype, c.d, s.ctas, stream);
 }
 

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttendParams p,
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.o) + row * D + lane * V);
 #pragma unroll
   for (int j = 0; j < V; j += 2) dst[j / 2] = pack2<T>(o[j] * inv * v, o[j + 1] * inv * v);
-  if (p.lse && lane == 0) p.lse[row] = (m - g.shift + log2f(l)) * kLn2;
+  if (p.lse && lane == 0) p.lse[row] = (m - kAttendShift + log2f(l)) * kLn2;
 }
 
 template <typename T>

@@ -41,7 +41,7 @@ constexpr int kKeys = 128;  // tokens of a key tile: what is converted at a time
 constexpr int kThreads = 640, kConvert = 256;
 constexpr int kIssue = 16, kPlan = 17;  // the warps that issue products and plan
 constexpr int kPlans = 4;               // units that the plan is ahead at most
-constexpr float kShift = kPromptShift;
+constexpr float kShift = kAttendShift;
 constexpr float kSlack = 8.f;  // growth of a row's maximum that is let pass
 constexpr int kMinTiles = 2;
 // registers of a thread after the split; 640 x 96 at launch

@@ -23,10 +23,11 @@
 //   converted tile in shared memory.
 // - q is scaled by a power of two for each row so that its largest entry lies in
 //   [2^14, 2^15) before it is rounded to f16: exact down to 2^-28 of the largest.
-// - Weights go to f16 as 2^15 p b_j / v, v the largest value scale so far
-//   (a power of two; the sums are rescaled when it or the maximum grows), so weights
-//   down to 2^-40 of the largest count.  Rounding them to f16 is 2^-11 each,
-//   of the size of the output's own rounding to fp16.
+// - Weights go to f16 as 2^7 p b_j / v, v the largest value scale so far (a power
+//   of two) and p relative to a reference maximum of the row that follows the true
+//   one only when that has grown by more than 2^8: the sums are rescaled then, or
+//   when v grows.  Weights down to 2^-32 of the largest count.  Rounding them to f16
+//   is 2^-11 each, of the size of the output's own rounding to fp16.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -41,19 +42,25 @@ namespace {
 constexpr int kTile = 64;        // tokens of a stage
 constexpr int kConsumers = 128;  // four warps
 constexpr int kThreads = kConsumers + 32;
-constexpr float kShift = kTokenShift;
+constexpr float kShift = kAttendShift;
+constexpr float kSlack = 8.f;   // growth of a row's maximum that is let pass
 constexpr int kMinTokenTiles = 2;
 
 template <int D, int MT>
 struct TokenLayout {
   static constexpr int kRows = 16 * MT;
-  static constexpr int kStages = D == 128 ? (MT == 1 ? 5 : 4) : 8;
+  // groups of 16 tokens that a warp takes at a time, and warps that share a stage
+  static constexpr int kSub = MT == 1 ? 2 : 1;
+  static constexpr int kSharers = 4 / kSub;
+  static constexpr int kStages = D == 128 ? (MT == 1 ? 4 : 3) : (MT == 1 ? 8 : 6);
+  // rows that the four warps' parts are put together for at a time
+  static constexpr int kMergeRows = 16;
   static constexpr int kHalf = kTile * D;             // bytes of a K or V tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kQOff = kStages * kStage;       // Q fragments
   static constexpr int kBufOff = kQOff + MT * (D / 16) * 512;
-  static constexpr int kBuf = kRows * (D + 4) * 4;     // one fp32 output tile, rows padded
-  static constexpr int kStatOff = kBufOff + 2 * kBuf;  // wm[4][rows], wl[4][rows], wv[4], rs[rows]
+  static constexpr int kBuf = kMergeRows * (D + 4) * 4;  // a warp's fp32 output, rows padded
+  static constexpr int kStatOff = kBufOff + 4 * kBuf;    // wm[4][rows], wl[4][rows], wv[4], rs[rows]
   static constexpr int kScaleOff = kStatOff + (9 * kRows + 4) * 4;  // float2 [stages][4]
   static constexpr int kBarOff = (kScaleOff + kStages * 4 * 8 + 7) / 8 * 8;
   static constexpr int kMiscOff = kBarOff + (2 * kStages + 1) * 8;  // scan scratch, start, abort
@@ -128,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   using L = TokenLayout<D, MT>;
   constexpr int KS = D / 16;  // 16-wide steps of q . k
   constexpr int NB = D / 8;   // 8-wide blocks of the output
+  constexpr int SUB = L::kSub;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 4);
+      mbar_init(&empty[i], L::kSharers);
     }
     mbar_init(consumers, 4);
     *abort_flag = 0;
@@ -271,46 +279,58 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto sync = [&]() { return warps_sync(consumers, syncs, p.status, abort_flag); };
   int4 tail = make_int4(0, 0, 0, 0);
   bool ok = true;
+  // The thread's share of a unit's q: eight threads a row, D / 8 values each.
+  constexpr int QV = D / 64;  // 16-byte pieces
+  uint4 qraw[MT][QV];
+  auto ask_q = [&](const Walk& u) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = mt * 16 + (threadIdx.x >> 3);
+      const int i = r / p.G, head = u.h * p.G + r % p.G;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          qg + (((int64_t)u.b * p.Hq + head) * p.N + i) * D + (threadIdx.x & 7) * (D / 8));
+#pragma unroll
+      for (int j = 0; j < QV; ++j)
+        qraw[mt][j] = r < u.nq * p.G ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  ask_q(w);
   while (w.pos < w.end && ok) {
     const int n = w.count();
     const int R = w.nq * p.G;
-    // q: rows as f16 operand pieces in shared memory, with each row's factor.
-    // Eight threads a row, D / 8 values each, two for each piece.
-    {
-      constexpr int V = D / 8;
+    // q: rows as f16 operand pieces in shared memory, with each row's factor.  The
+    // sign of the scale goes into q, so that the factor is not negative.
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int r = mt * 16 + (threadIdx.x >> 3), e = threadIdx.x & 7;
-        float x[V];
-        float top = 0.f;
-        if (r < R) {
-          const int i = r / p.G, head = w.h * p.G + r % p.G;
-          const T* src = qg + (((int64_t)w.b * p.Hq + head) * p.N + i) * D + e * V;
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = mt * 16 + (threadIdx.x >> 3), e = threadIdx.x & 7;
+      float x[D / 8];
+      float top = 0.f;
 #pragma unroll
-          for (int j = 0; j < V; j += 8) load8<T>(src + j, *reinterpret_cast<float(*)[8]>(x + j));
-        } else {
+      for (int j = 0; j < QV; ++j) {
+        const uint32_t u[4] = {qraw[mt][j].x, qraw[mt][j].y, qraw[mt][j].z, qraw[mt][j].w};
 #pragma unroll
-          for (int j = 0; j < V; ++j) x[j] = 0.f;
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = unpack2<T>(u[k]);
+          x[8 * j + 2 * k] = f.x;
+          x[8 * j + 2 * k + 1] = f.y;
+          top = max3(top, fabsf(f.x), fabsf(f.y));
         }
+      }
 #pragma unroll
-        for (int j = 0; j < V; ++j) top = fmaxf(top, fabsf(x[j]));
+      for (int k = 4; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      // largest entry into [2^14, 2^15); rows of zeros, infinities and NaN as they are
+      const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+      const float up = top > 0.f && ex < 128 ? pow2i(max(min(14 - ex, 127), -126)) : 1.f;
+      if (e == 0) rs[r] = fabsf(p.scale) * kLog2e / up;
+      const float f = p.scale < 0.f ? -up : up;
 #pragma unroll
-        for (int m = 4; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        // largest entry into [2^14, 2^15); rows of zeros, infinities and NaN as they are
-        const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-        const bool scaled = top > 0.f && ex < 128;
-        const int up = scaled ? min(14 - ex, 127) : 0;
-        const float f = scaled ? __uint_as_float((uint32_t)(max(up, -126) + 127) << 23) : 1.f;
-        if (e == 0) rs[r] = p.scale * kLog2e / f;
-#pragma unroll
-        for (int j = 0; j < V; j += 2) {
-          const int d = e * V + j;
-          const int cc = d / (D / 4), ks = (d % (D / 4)) / 4, pair = (d & 3) >> 1;
-          const uint32_t at = sq + (((mt * KS + ks) * 32 + (r & 7) * 4 + cc) * 16) +
-                              (pair * 2 + ((r >> 3) & 1)) * 4;
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack2<__half>(x[j] * f, x[j + 1] * f))
-                       : "memory");
-        }
+      for (int j = 0; j < D / 8; j += 2) {
+        const int d = e * (D / 8) + j;
+        const int cc = d / (D / 4), ks = (d % (D / 4)) / 4, pair = (d & 3) >> 1;
+        const uint32_t at = sq + (((mt * KS + ks) * 32 + (r & 7) * 4 + cc) * 16) +
+                            (pair * 2 + ((r >> 3) & 1)) * 4;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack2<__half>(x[j] * f, x[j + 1] * f))
+                     : "memory");
       }
     }
     if (!(ok = sync())) break;
@@ -335,127 +355,115 @@ __global__ void __launch_bounds__(kThreads, 2)
     float vref = 0.f, vinv = 0.f;
 
     for (int i = 0; i < n; ++i, ++it) {
+      if (SUB == 2 && ((i ^ (warp >> 1)) & 1)) continue;  // the other two warps' stage
       const int s = it % L::kStages;
       ok = warp_wait(&full[s], (it / L::kStages) & 1, p.status, abort_flag);
       if (!ok) break;
-      const int t0 = (w.tile + i) * kTile + warp * 16;  // first of this warp's 16 tokens
+      const int g0 = (warp % L::kSharers) * SUB;          // first of this warp's groups
+      const int t0 = (w.tile + i) * kTile + g0 * 16;      // and its first token
       if (t0 >= w.kv) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
         continue;
       }
-      const float2 sc = sscale[s * 4 + warp];
-      const uint32_t kb = base + s * L::kStage + warp * 16 * D, vb = kb + L::kHalf;
-      // scores: 16 rows x 16 tokens for each row block
-      float sr[MT][2][4];
+      float2 sc[SUB];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) sc[u] = sscale[s * 4 + g0 + u];
+      const uint32_t kb = base + s * L::kStage + g0 * 16 * D, vb = kb + L::kHalf;
+      // rows of the stage that hold no token, or a page that is not known (or, behind
+      // the last token, was not copied): codes of zero
+      const bool edge = t0 + 16 * SUB > w.kv || sc[0].x < 0.f || sc[SUB - 1].x < 0.f;
+      // scores: 16 rows x 16 tokens for each row block and group
+      float sr[MT][2 * SUB][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+        for (int nb = 0; nb < 2 * SUB; ++nb)
 #pragma unroll
           for (int k = 0; k < 4; ++k) sr[mt][nb][k] = 0.f;
-      uint32_t kw[2][KS];
+      {
+        uint32_t kw[2 * SUB][KS];
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const int row = nb * 8 + g;  // of the warp's 16 (a multiple of 8 rows into the tile)
-        if constexpr (D == 128) {
-          const uint4 x = lds128(kb + row * D + (((2 * c) ^ g) << 4));
-          const uint4 y = lds128(kb + row * D + (((2 * c + 1) ^ g) << 4));
-          kw[nb][0] = x.x; kw[nb][1] = x.y; kw[nb][2] = x.z; kw[nb][3] = x.w;
-          kw[nb][4] = y.x; kw[nb][5] = y.y; kw[nb][6] = y.z; kw[nb][7] = y.w;
-        } else {
-          const uint4 x = lds128(kb + row * D + ((c ^ ((g >> 1) & 3)) << 4));
-          kw[nb][0] = x.x; kw[nb][1] = x.y; kw[nb][2] = x.z; kw[nb][3] = x.w;
+        for (int nb = 0; nb < 2 * SUB; ++nb) {
+          const int row = nb * 8 + g;  // of the warp's tokens (a multiple of 8 rows into the tile)
+          if constexpr (D == 128) {
+            const uint4 x = lds128(kb + row * D + (((2 * c) ^ g) << 4));
+            const uint4 y = lds128(kb + row * D + (((2 * c + 1) ^ g) << 4));
+            kw[nb][0] = x.x; kw[nb][1] = x.y; kw[nb][2] = x.z; kw[nb][3] = x.w;
+            kw[nb][4] = y.x; kw[nb][5] = y.y; kw[nb][6] = y.z; kw[nb][7] = y.w;
+          } else {
+            const uint4 x = lds128(kb + row * D + ((c ^ ((g >> 1) & 3)) << 4));
+            kw[nb][0] = x.x; kw[nb][1] = x.y; kw[nb][2] = x.z; kw[nb][3] = x.w;
+          }
         }
-      }
-      // values: tokens 2c, 2c + 1, 2c + 8, 2c + 9, D / 8 numbers each from (D / 8) g on
-      uint32_t vw[4][D / 32];
+        if (edge) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int row = 2 * c + (k & 1) + (k >> 1) * 8;
-        if constexpr (D == 128) {
-          const uint4 x = lds128(vb + row * D + ((g ^ (row & 7)) << 4));
-          vw[k][0] = x.x; vw[k][1] = x.y; vw[k][2] = x.z; vw[k][3] = x.w;
-        } else {
-          const uint2 x = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-          vw[k][0] = x.x; vw[k][1] = x.y;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
-      const bool edge = t0 + 16 > w.kv || sc.x < 0.f;  // rows of the tile that hold no token
-      if (edge) {
+          for (int nb = 0; nb < 2 * SUB; ++nb)
+            if (sc[nb / 2].x < 0.f)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (sc.x < 0.f || t0 + 2 * c + (k & 1) + (k >> 1) * 8 >= w.kv)
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) vw[k][j] = 0u;
-        if (sc.x < 0.f)
-#pragma unroll
-          for (int j = 0; j < KS; ++j) kw[0][j] = kw[1][j] = 0u;
-      }
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint32_t kf[2][2];
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          kf[nb][0] = e4m3x2_to_f16x2(kw[nb][ks] & 0xffffu);
-          kf[nb][1] = e4m3x2_to_f16x2(kw[nb][ks] >> 16);
+              for (int j = 0; j < KS; ++j) kw[nb][j] = 0u;
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint4 a = lds128(sq + ((mt * KS + ks) * 32 + lane) * 16);
-          mma16816(sr[mt][0], a, kf[0][0], kf[0][1]);
-          mma16816(sr[mt][1], a, kf[1][0], kf[1][1]);
+        for (int ks = 0; ks < KS; ++ks) {
+          uint4 a[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) a[mt] = lds128(sq + ((mt * KS + ks) * 32 + lane) * 16);
+#pragma unroll
+          for (int nb = 0; nb < 2 * SUB; ++nb) {
+            const uint32_t k0 = e4m3x2_to_f16x2(kw[nb][ks]), k1 = e4m3x2_to_f16x2(kw[nb][ks] >> 16);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma16816(sr[mt][nb], a[mt], k0, k1);
+          }
         }
       }
       // value scales: a larger one than before makes the sums relative to it
       float grow = 1.f;
-      if (sc.y > vref) {
-        grow = vref / sc.y;
-        vref = sc.y;
+      const float vtop = fmaxf(sc[0].y, sc[SUB - 1].y);
+      if (vtop > vref) {
+        grow = vref / vtop;
+        vref = vtop;
         vinv = 1.f / vref;
       }
-      const float vf = sc.y * vinv;
-      const float kf = fmaxf(sc.x, 0.f);
-      const bool hidden = t0 + 15 > w.kv - w.nq;  // some row does not see some token
-      uint4 pa[MT];
+      if (t0 + 16 * SUB - 1 > w.kv - w.nq) {  // some row does not see some token
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nb = 0; nb < 2 * SUB; ++nb)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (t0 + nb * 8 + 2 * c + (k & 1) > last[mt][k >> 1]) sr[mt][nb][k] = -INFINITY;
+      }
+      uint4 pa[MT][SUB];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float pr[2][4], a[2];
+        // a row's new reference maximum, where it has grown past the slack
+        float f[SUB][2];
+        bool grows = grow != 1.f;
+        float mx[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float f = rf[mt][k] * kf;
-          float mx = m[mt][k];
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float x = sr[mt][nb][2 * k + j] * f;
-              if (hidden && t0 + nb * 8 + 2 * c + j > last[mt][k]) x = -INFINITY;
-              pr[nb][2 * k + j] = x;
-              mx = fmaxf(mx, x);
-            }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float ref = mx == -INFINITY ? 0.f : mx;
-          a[k] = exp2_fast(m[mt][k] - ref);
-          m[mt][k] = mx;
-          float sum = 0.f;
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float e = exp2_fast(pr[nb][2 * k + j] - ref + kShift);
-              sum += e;
-              pr[nb][2 * k + j] = e * vf;
-            }
-          l[mt][k] = l[mt][k] * a[k] + sum;
-          a[k] *= grow;
+          for (int u = 0; u < SUB; ++u) {
+            // (not zero: a masked score stays at -infinity)
+            f[u][k] = fmaxf(rf[mt][k] * sc[u].x, 1.17549435e-38f);
+            const float top = fmaxf(max3(sr[mt][2 * u][2 * k], sr[mt][2 * u][2 * k + 1],
+                                         sr[mt][2 * u + 1][2 * k]), sr[mt][2 * u + 1][2 * k + 1]);
+            mx[k] = u ? fmaxf(mx[k], top * f[u][k]) : top * f[u][k];
+          }
+          grows |= mx[k] > m[mt][k] + kSlack || (m[mt][k] == -INFINITY && mx[k] > -INFINITY);
         }
-        pa[mt] = make_uint4(pack2<__half>(pr[0][0], pr[0][1]), pack2<__half>(pr[0][2], pr[0][3]),
-                            pack2<__half>(pr[1][0], pr[1][1]), pack2<__half>(pr[1][2], pr[1][3]));
-        if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+        if (__any_sync(0xffffffffu, grows)) {
+          float a[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+            const bool up = mx[k] > m[mt][k];  // of the whole row, once any lane of the warp asks
+            a[k] = up ? exp2_fast(m[mt][k] - mx[k]) : 1.f;
+            if (up) m[mt][k] = mx[k];
+            l[mt][k] *= a[k];
+            a[k] *= grow;
+          }
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             o[mt][j][0] *= a[0];
@@ -464,96 +472,141 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[mt][j][3] *= a[1];
           }
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float off = kShift - (m[mt][k] == -INFINITY ? 0.f : m[mt][k]);
+          float sum = 0.f;
+#pragma unroll
+          for (int nb = 0; nb < 2 * SUB; ++nb) {
+            const float vf = sc[nb / 2].y * vinv;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float e = exp2_fast(fmaf(sr[mt][nb][2 * k + j], f[nb / 2][k], off));
+              sum += e;
+              sr[mt][nb][2 * k + j] = e * vf;
+            }
+          }
+          l[mt][k] += sum;
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const float(&x)[4] = sr[mt][2 * u], (&y)[4] = sr[mt][2 * u + 1];
+          pa[mt][u] = make_uint4(pack2<__half>(x[0], x[1]), pack2<__half>(x[2], x[3]),
+                                 pack2<__half>(y[0], y[1]), pack2<__half>(y[2], y[3]));
+        }
       }
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const uint32_t t01a = __byte_perm(vw[0][j], vw[1][j], 0x5140);
-        const uint32_t t01b = __byte_perm(vw[0][j], vw[1][j], 0x7362);
-        const uint32_t t23a = __byte_perm(vw[2][j], vw[3][j], 0x5140);
-        const uint32_t t23b = __byte_perm(vw[2][j], vw[3][j], 0x7362);
-        const uint32_t b0[4] = {e4m3x2_to_f16x2(t01a & 0xffffu), e4m3x2_to_f16x2(t01a >> 16),
-                                e4m3x2_to_f16x2(t01b & 0xffffu), e4m3x2_to_f16x2(t01b >> 16)};
-        const uint32_t b1[4] = {e4m3x2_to_f16x2(t23a & 0xffffu), e4m3x2_to_f16x2(t23a >> 16),
-                                e4m3x2_to_f16x2(t23b & 0xffffu), e4m3x2_to_f16x2(t23b >> 16)};
+      for (int u = 0; u < SUB; ++u) {
+        // values: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of the group, D / 8 numbers each
+        // from (D / 8) g on
+        uint32_t vw[4][D / 32];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) {
+          const int row = u * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 x = lds128(vb + row * D + ((g ^ (row & 7)) << 4));
+            vw[k][0] = x.x; vw[k][1] = x.y; vw[k][2] = x.z; vw[k][3] = x.w;
+          } else {
+            const uint2 x = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+            vw[k][0] = x.x; vw[k][1] = x.y;
+          }
+        }
+        if (edge) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * j + k], pa[mt], b0[k], b1[k]);
+          for (int k = 0; k < 4; ++k)
+            if (sc[u].x < 0.f || t0 + u * 16 + 2 * c + (k & 1) + (k >> 1) * 8 >= w.kv)
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) vw[k][j] = 0u;
+        }
+        if (u == SUB - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[s]);
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint32_t t01a = __byte_perm(vw[0][j], vw[1][j], 0x5140);
+          const uint32_t t01b = __byte_perm(vw[0][j], vw[1][j], 0x7362);
+          const uint32_t t23a = __byte_perm(vw[2][j], vw[3][j], 0x5140);
+          const uint32_t t23b = __byte_perm(vw[2][j], vw[3][j], 0x7362);
+          const uint32_t b0[4] = {e4m3x2_to_f16x2(t01a), e4m3x2_to_f16x2(t01a >> 16),
+                                  e4m3x2_to_f16x2(t01b), e4m3x2_to_f16x2(t01b >> 16)};
+          const uint32_t b1[4] = {e4m3x2_to_f16x2(t23a), e4m3x2_to_f16x2(t23a >> 16),
+                                  e4m3x2_to_f16x2(t23b), e4m3x2_to_f16x2(t23b >> 16)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * j + k], pa[mt][u], b0[k], b1[k]);
+        }
       }
     }
     if (!ok) break;
 
-    // the four warps' parts of the unit into one
+    // the next unit's q on its way, the four warps' parts of this one into one: each
+    // writes its own, and all threads add them up
+    Walk nx = w;
+    nx.next(p);
+    if (nx.pos < nx.end) ask_q(nx);
+    const bool begins = w.tile == 0, ends = w.tile + n == w.tiles;
+    float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * L::kRows * (D + kPartStats);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt * 16 >= R) break;
+      if (mt && !(ok = sync())) break;  // the rows before have been read
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 1);
         l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 2);
+        const int r = k * 8 + g;
+        if (mt * 16 + r >= R) continue;
         if (c == 0) {
-          wm[warp * L::kRows + mt * 16 + k * 8 + g] = m[mt][k];
-          wl[warp * L::kRows + mt * 16 + k * 8 + g] = l[mt][k];
+          wm[warp * L::kRows + r] = m[mt][k];
+          wl[warp * L::kRows + r] = l[mt][k];
         }
+        // piece j / 4 of column block 2c + jj: no two lanes of a store on one bank
+        float* at = buf + warp * (L::kBuf / 4) + r * (D + 4) + 2 * c * 4;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+          for (int j = 0; j < NB; j += 4)
+            *reinterpret_cast<float4*>(at + (j / 4) * 32 + jj * 4) =
+                make_float4(o[mt][j][2 * k + jj], o[mt][j + 1][2 * k + jj], o[mt][j + 2][2 * k + jj],
+                            o[mt][j + 3][2 * k + jj]);
       }
-    if (lane == 0) wv[warp] = vref;
-    if (!(ok = sync())) break;
-    const float vmax = fmaxf(fmaxf(wv[0], wv[1]), fmaxf(wv[2], wv[3]));
-    auto row_max = [&](int r) {
-      return fmaxf(fmaxf(wm[r], wm[L::kRows + r]), fmaxf(wm[2 * L::kRows + r], wm[3 * L::kRows + r]));
-    };
-    const float vpart = vmax > 0.f ? vref / vmax : 0.f;
-    auto each = [&](auto&& f) {  // f(row, column, value) over this thread's part
+      if (lane == 0) wv[warp] = vref;
+      if (!(ok = sync())) break;
+      const float vmax = fmaxf(fmaxf(wv[0], wv[1]), fmaxf(wv[2], wv[3]));
+      const float vdiv = vmax > 0.f ? 1.f / vmax : 0.f;
+      for (int e = threadIdx.x; e < min(16, R - mt * 16) * (D / 4); e += kConsumers) {
+        const int r = e / (D / 4), d4 = e % (D / 4), rr = mt * 16 + r;
+        const float mx = fmaxf(max3(wm[r], wm[L::kRows + r], wm[2 * L::kRows + r]), wm[3 * L::kRows + r]);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = mt * 16 + k * 8 + g;
-          const float mx = row_max(r);
-          const float a = exp2_fast(m[mt][k] - (mx == -INFINITY ? 0.f : mx)) * vpart;
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-            for (int j = 0; j < NB; j += 4)
-              f(buf + (warp & 1) * (L::kBuf / 4) + r * (D + 4) + (2 * c + jj) * NB + j,
-                make_float4(o[mt][j][2 * k + jj] * a, o[mt][j + 1][2 * k + jj] * a,
-                            o[mt][j + 2][2 * k + jj] * a, o[mt][j + 3][2 * k + jj] * a));
+        for (int k = 0; k < 4; ++k) {
+          const float a = exp2_fast(wm[k * L::kRows + r] - ref), b = a * (wv[k] * vdiv);
+          const float4 x = *reinterpret_cast<const float4*>(
+              buf + k * (L::kBuf / 4) + r * (D + 4) + (d4 % (NB / 4)) * 32 + d4 / (NB / 4) * 4);
+          sum += wl[k * L::kRows + r] * a;
+          z = make_float4(z.x + x.x * b, z.y + x.y * b, z.z + x.z * b, z.w + x.w * b);
         }
-    };
-    if (warp >= 2) each([](float* at, float4 x) { *reinterpret_cast<float4*>(at) = x; });
-    if (!(ok = sync())) break;
-    if (warp < 2)
-      each([](float* at, float4 x) {
-        float4* y = reinterpret_cast<float4*>(at);
-        const float4 z = *y;
-        *y = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
-      });
-    if (!(ok = sync())) break;
-    const bool begins = w.tile == 0, ends = w.tile + n == w.tiles;
-    float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * L::kRows * (D + kPartStats);
-    for (int e = threadIdx.x; e < R * (D / 4); e += kConsumers) {
-      const int r = e / (D / 4), d4 = e % (D / 4);
-      const float4 x = *reinterpret_cast<float4*>(buf + r * (D + 4) + d4 * 4);
-      const float4 y = *reinterpret_cast<float4*>(buf + L::kBuf / 4 + r * (D + 4) + d4 * 4);
-      float4 z = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-      const float mx = row_max(r), ref = mx == -INFINITY ? 0.f : mx;
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum += wl[k * L::kRows + r] * exp2_fast(wm[k * L::kRows + r] - ref);
-      if (begins && ends) {
-        const int i = r / p.G, head = w.h * p.G + r % p.G;
-        const int64_t row = ((int64_t)w.b * p.Hq + head) * p.N + i;
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;
-        uint2 out;
-        out.x = pack2<T>(z.x * inv * vmax, z.y * inv * vmax);
-        out.y = pack2<T>(z.z * inv * vmax, z.w * inv * vmax);
-        *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + row * D + d4 * 4) = out;
-        if (p.lse && d4 == 0) p.lse[row] = (mx - kShift + log2f(sum)) * kLn2;
-      } else {
-        reinterpret_cast<float4*>(part)[r * (D / 4) + d4] = z;
-        if (d4 == 0)
-          reinterpret_cast<float4*>(part + L::kRows * D)[r] = make_float4(mx, sum, vmax, 0.f);
+        if (begins && ends) {
+          const int i = rr / p.G, head = w.h * p.G + rr % p.G;
+          const int64_t row = ((int64_t)w.b * p.Hq + head) * p.N + i;
+          const float inv = sum != 0.f ? 1.f / sum : 0.f;
+          uint2 out;
+          out.x = pack2<T>(z.x * inv * vmax, z.y * inv * vmax);
+          out.y = pack2<T>(z.z * inv * vmax, z.w * inv * vmax);
+          *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + row * D + d4 * 4) = out;
+          if (p.lse && d4 == 0) p.lse[row] = (mx - kShift + log2f(sum)) * kLn2;
+        } else {
+          reinterpret_cast<float4*>(part)[rr * (D / 4) + d4] = z;
+          if (d4 == 0)
+            reinterpret_cast<float4*>(part + L::kRows * D)[rr] = make_float4(mx, sum, vmax, 0.f);
+        }
       }
     }
+    if (!ok) break;
     if (begins && !ends) {
       // blocks that hold the rest: the share of block k ends at total (k + 1) / shares
       const int64_t unit_end = w.pos + w.tiles;
@@ -562,8 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       while (total * (k + 1) / shares < unit_end) ++k;
       tail = make_int4(k - (int)blockIdx.x, w.b, w.h, 0);
     }
-    if (!(ok = sync())) break;
-    w.next(p);
+    w = nx;  // (what this unit left in shared memory is written again after the next sync)
   }
   if (threadIdx.x == 0) p.tails[blockIdx.x] = ok ? tail : make_int4(0, 0, 0, 0);
   griddep_launch_dependents();
