@@ -15,11 +15,11 @@ struct Shape {
   int ctas, rows;  // blocks, rows of a part
 };
 
-Shape shape_of(int G, int64_t N, int sms) {
+Shape shape_of(int G, int64_t N, int d, int sms) {
   Shape s;
   s.token = N * G <= kTokenRows;
   s.rows = s.token ? (N * G <= 16 ? 16 : 32) : 256;
-  s.ctas = s.token ? 2 * sms : sms;
+  s.ctas = s.token ? (d == 128 ? 2 : 3) * sms : sms;
   return s;
 }
 
@@ -34,7 +34,7 @@ cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype
                                 void* o, float* lse, int B, int Hq, int64_t N, int max_pages,
                                 float scale, void* workspace, unsigned* status, int sms,
                                 cudaStream_t stream) {
-  const Shape s = shape_of(Hq / c.Hkv, N, sms);
+  const Shape s = shape_of(Hq / c.Hkv, N, c.d, sms);
   AttendParams p{q, {c.k_codes, c.v_codes}, {c.k_scale, c.v_scale}, table, kv_len, q_len, o,
                  lse, status, N, c.num_pages, B, Hq, c.Hkv, Hq / c.Hkv, max_pages,
                  page_log2(c.page), scale, static_cast<float*>(workspace), nullptr};
@@ -49,7 +49,7 @@ cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype
 }
 
 size_t attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d, int sms) {
-  const Shape s = shape_of(Hq / Hkv, N, sms);
+  const Shape s = shape_of(Hq / Hkv, N, d, sms);
   return (part_bytes(s, d) + (size_t)s.ctas * sizeof(int4) + 255) / 256 * 256;
 }
 

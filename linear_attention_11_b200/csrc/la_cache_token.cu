@@ -46,24 +46,27 @@ constexpr float kShift = kAttendShift;
 constexpr float kSlack = 8.f;   // growth of a row's maximum that is let pass
 constexpr int kMinTokenTiles = 2;
 
-template <int D, int MT>
+// RG row groups of 16 rows: with one, two warps take a stage's 64 tokens, 32 each,
+// and the other two the next stage's; with two, all four take every stage, two for each
+// row group (a warp that held both groups' outputs would not fit its registers: rows
+// 32, 32 x 8 heads, up to 8192 tokens, 158 us against XX).
+template <int D, int RG>
 struct TokenLayout {
-  static constexpr int kRows = 16 * MT;
-  // groups of 16 tokens that a warp takes at a time, and warps that share a stage
-  static constexpr int kSub = MT == 1 ? 2 : 1;
-  static constexpr int kSharers = 4 / kSub;
-  static constexpr int kStages = D == 128 ? (MT == 1 ? 4 : 3) : (MT == 1 ? 8 : 6);
-  // rows that the four warps' parts are put together for at a time
-  static constexpr int kMergeRows = 16;
+  static constexpr int kRows = 16 * RG;
+  static constexpr int kSub = 2;           // groups of 16 tokens that a warp takes at a time
+  static constexpr int kSharers = 2 * RG;  // warps that read a stage
+  static constexpr int kStages = D == 128 ? 5 - RG : 7 - RG;
   static constexpr int kHalf = kTile * D;             // bytes of a K or V tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kQOff = kStages * kStage;       // Q fragments
-  static constexpr int kBufOff = kQOff + MT * (D / 16) * 512;
-  static constexpr int kBuf = kMergeRows * (D + 4) * 4;  // a warp's fp32 output, rows padded
-  static constexpr int kStatOff = kBufOff + 4 * kBuf;    // wm[4][rows], wl[4][rows], wv[4], rs[rows]
-  static constexpr int kScaleOff = kStatOff + (9 * kRows + 4) * 4;  // float2 [stages][4]
+  static constexpr int kRawOff = kQOff + RG * (D / 16) * 512;  // two units' q as they come
+  static constexpr int kRaw = kRows * D * 2;
+  static constexpr int kBufOff = kRawOff + 2 * kRaw;
+  static constexpr int kBuf = 16 * (D + 4) * 4;         // a warp's fp32 output, rows padded
+  static constexpr int kStatOff = kBufOff + 4 * kBuf;    // wm[4][16], wl[4][16], wv[4], rs[rows]
+  static constexpr int kScaleOff = kStatOff + (8 * 16 + 4 + kRows) * 4;  // float2 [stages][4]
   static constexpr int kBarOff = (kScaleOff + kStages * 4 * 8 + 7) / 8 * 8;
-  static constexpr int kMiscOff = kBarOff + (2 * kStages + 1) * 8;  // scan scratch, start, abort
+  static constexpr int kMiscOff = kBarOff + (2 * kStages + 5) * 8;  // scan scratch, start, abort
   static constexpr int kBytes = kMiscOff + 128 + 1024;        // + slack to align to 1024
 };
 
@@ -93,6 +96,15 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -127,12 +139,12 @@ struct Walk {
   }
 };
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int D, int RG>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     token_kernel(const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const AttendParams p, int box,
                  int min_tiles) {
-  using L = TokenLayout<D, MT>;
+  using L = TokenLayout<D, RG>;
   constexpr int KS = D / 16;  // 16-wide steps of q . k
   constexpr int NB = D / 8;   // 8-wide blocks of the output
   constexpr int SUB = L::kSub;
@@ -141,13 +153,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* sm = smem_raw + (base - raw);
   float* buf = reinterpret_cast<float*>(sm + L::kBufOff);
   float* wm = reinterpret_cast<float*>(sm + L::kStatOff);
-  float* wl = wm + 4 * L::kRows;
-  float* rs = wl + 4 * L::kRows;
-  float* wv = rs + L::kRows;
+  float* wl = wm + 4 * 16;
+  float* wv = wl + 4 * 16;
+  float* rs = wv + 4;
   float2* sscale = reinterpret_cast<float2*>(sm + L::kScaleOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBarOff);
   uint64_t* empty = full + L::kStages;
-  uint64_t* consumers = empty + L::kStages;  // a barrier of the four warps
+  uint64_t* q_full = empty + L::kStages;     // [2] a unit's q has come; it has been read
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* consumers = q_empty + 2;         // a barrier of the four warps
   int64_t* misc = reinterpret_cast<int64_t*>(sm + L::kMiscOff);  // [0, 5) scan, then the start
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 12);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,6 +170,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], L::kSharers);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 4);
     }
     mbar_init(consumers, 4);
     *abort_flag = 0;
@@ -213,8 +231,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t bytes = (uint32_t)box * D;
     int it = 0;
     bool go = true;
-    while (w.pos < w.end && go) {
+    int unit = 0, asked = 0;  // units; units whose q has been asked for
+    for (; w.pos < w.end && go; ++unit) {
       const int n = w.count();
+      {  // q: a row for each lane
+        const int R = w.nq * p.G, qs = unit & 1;
+        if (unit >= 2) go = warp_wait(&q_empty[qs], ((unit >> 1) - 1) & 1, p.status, abort_flag);
+        if (!go) break;
+        if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)R * D * 2);
+        asked = unit + 1;
+        __syncwarp();
+        if (lane < R) {
+          const int64_t row = ((int64_t)w.b * p.Hq + w.h * p.G + lane % p.G) * p.N + lane / p.G;
+          bulk_load(base + L::kRawOff + qs * L::kRaw + lane * D * 2,
+                    static_cast<const T*>(p.q) + row * D, D * 2, &q_full[qs]);
+        }
+      }
       const int* row = p.table + (int64_t)w.b * p.max_pages;
       auto page_at = [&](int group) {  // page of 16-token group `group` of the unit (-2: none)
         return (int64_t)group * 16 < w.kv ? row[group >> (p.page_log2 - 4)] : -2;
@@ -267,47 +299,38 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (*abort_flag) {  // let copies already issued land before the block exits
       for (int k = max(0, it - L::kStages); k < it; ++k)
         mbar_wait_drain(&full[k % L::kStages], (k / L::kStages) & 1);
+      for (int k = max(0, unit - 1); k <= unit; ++k)
+        if (k < asked) mbar_wait_drain(&q_full[k & 1], (k >> 1) & 1);
     }
     return;
   }
 
   // -------------------------------------------------------------- products
-  const int g = lane >> 2, c = lane & 3;
+  const int g = lane >> 2, c = lane & 3, rg = RG == 2 ? warp >> 1 : 0;
   const uint32_t sq = base + L::kQOff;
-  const T* qg = static_cast<const T*>(p.q);
   int it = 0, syncs = 0;
   auto sync = [&]() { return warps_sync(consumers, syncs, p.status, abort_flag); };
   int4 tail = make_int4(0, 0, 0, 0);
   bool ok = true;
-  // The thread's share of a unit's q: eight threads a row, D / 8 values each.
-  constexpr int QV = D / 64;  // 16-byte pieces
-  uint4 qraw[MT][QV];
-  auto ask_q = [&](const Walk& u) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = mt * 16 + (threadIdx.x >> 3);
-      const int i = r / p.G, head = u.h * p.G + r % p.G;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          qg + (((int64_t)u.b * p.Hq + head) * p.N + i) * D + (threadIdx.x & 7) * (D / 8));
-#pragma unroll
-      for (int j = 0; j < QV; ++j)
-        qraw[mt][j] = r < u.nq * p.G ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  ask_q(w);
-  while (w.pos < w.end && ok) {
+  int unit = 0;
+  for (; w.pos < w.end && ok; ++unit) {
     const int n = w.count();
     const int R = w.nq * p.G;
-    // q: rows as f16 operand pieces in shared memory, with each row's factor.  The
-    // sign of the scale goes into q, so that the factor is not negative.
+    ok = warp_wait(&q_full[unit & 1], (unit >> 1) & 1, p.status, abort_flag);
+    if (!ok) break;
+    // q: rows as f16 operand pieces in shared memory, with each row's factor.  Eight
+    // threads a row, D / 8 values each.  The sign of the scale goes into q, so that
+    // the factor is not negative.
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int mt = 0; mt < RG; ++mt) {
       const int r = mt * 16 + (threadIdx.x >> 3), e = threadIdx.x & 7;
       float x[D / 8];
       float top = 0.f;
 #pragma unroll
-      for (int j = 0; j < QV; ++j) {
-        const uint32_t u[4] = {qraw[mt][j].x, qraw[mt][j].y, qraw[mt][j].z, qraw[mt][j].w};
+      for (int j = 0; j < D / 64; ++j) {
+        uint4 q4 = make_uint4(0u, 0u, 0u, 0u);
+        if (r < R) q4 = lds128(base + L::kRawOff + (unit & 1) * L::kRaw + r * D * 2 + e * (D / 4) + j * 16);
+        const uint32_t u[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = unpack2<T>(u[k]);
@@ -333,33 +356,34 @@ __global__ void __launch_bounds__(kThreads, 2)
                      : "memory");
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_empty[unit & 1]);
     if (!(ok = sync())) break;
 
-    float o[MT][NB][4], m[MT][2], l[MT][2], rf[MT][2];
-    int last[MT][2];  // last token that the row sees
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    float o[NB][4], m[2], l[2], rf[2];
+    int last[2];  // last token that the row sees
+    {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int r = mt * 16 + k * 8 + g;
-        m[mt][k] = -INFINITY;
-        l[mt][k] = 0.f;
-        rf[mt][k] = rs[r];
-        last[mt][k] = r < R ? w.kv - w.nq + r / p.G : w.kv - 1;
+        const int r = rg * 16 + k * 8 + g;
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+        rf[k] = rs[r];
+        last[k] = r < R ? w.kv - w.nq + r / p.G : w.kv - 1;
       }
 #pragma unroll
       for (int j = 0; j < NB; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[mt][j][k] = 0.f;
+        for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
     }
     float vref = 0.f, vinv = 0.f;
 
     for (int i = 0; i < n; ++i, ++it) {
-      if (SUB == 2 && ((i ^ (warp >> 1)) & 1)) continue;  // the other two warps' stage
+      if (RG == 1 && ((i ^ (warp >> 1)) & 1)) continue;  // the other two warps' stage
       const int s = it % L::kStages;
       ok = warp_wait(&full[s], (it / L::kStages) & 1, p.status, abort_flag);
       if (!ok) break;
-      const int g0 = (warp % L::kSharers) * SUB;          // first of this warp's groups
+      const int g0 = (warp & 1) * SUB;          // first of this warp's groups
       const int t0 = (w.tile + i) * kTile + g0 * 16;      // and its first token
       if (t0 >= w.kv) {
         __syncwarp();
@@ -374,13 +398,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       // the last token, was not copied): codes of zero
       const bool edge = t0 + 16 * SUB > w.kv || sc[0].x < 0.f || sc[SUB - 1].x < 0.f;
       // scores: 16 rows x 16 tokens for each row block and group
-      float sr[MT][2 * SUB][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      float sr[2 * SUB][4];
 #pragma unroll
         for (int nb = 0; nb < 2 * SUB; ++nb)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sr[mt][nb][k] = 0.f;
+          for (int k = 0; k < 4; ++k) sr[nb][k] = 0.f;
       {
         uint32_t kw[2 * SUB][KS];
 #pragma unroll
@@ -405,14 +427,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          uint4 a[MT];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) a[mt] = lds128(sq + ((mt * KS + ks) * 32 + lane) * 16);
+          const uint4 a = lds128(sq + ((rg * KS + ks) * 32 + lane) * 16);
 #pragma unroll
           for (int nb = 0; nb < 2 * SUB; ++nb) {
             const uint32_t k0 = e4m3x2_to_f16x2(kw[nb][ks]), k1 = e4m3x2_to_f16x2(kw[nb][ks] >> 16);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(sr[mt][nb], a[mt], k0, k1);
+            mma16816(sr[nb], a, k0, k1);
           }
         }
       }
@@ -426,16 +445,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (t0 + 16 * SUB - 1 > w.kv - w.nq) {  // some row does not see some token
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
           for (int nb = 0; nb < 2 * SUB; ++nb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (t0 + nb * 8 + 2 * c + (k & 1) > last[mt][k >> 1]) sr[mt][nb][k] = -INFINITY;
+              if (t0 + nb * 8 + 2 * c + (k & 1) > last[k >> 1]) sr[nb][k] = -INFINITY;
       }
-      uint4 pa[MT][SUB];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      uint4 pa[SUB];
+      {
         // a row's new reference maximum, where it has grown past the slack
         float f[SUB][2];
         bool grows = grow != 1.f;
@@ -445,12 +461,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int u = 0; u < SUB; ++u) {
             // (not zero: a masked score stays at -infinity)
-            f[u][k] = fmaxf(rf[mt][k] * sc[u].x, 1.17549435e-38f);
-            const float top = fmaxf(max3(sr[mt][2 * u][2 * k], sr[mt][2 * u][2 * k + 1],
-                                         sr[mt][2 * u + 1][2 * k]), sr[mt][2 * u + 1][2 * k + 1]);
+            f[u][k] = fmaxf(rf[k] * sc[u].x, 1.17549435e-38f);
+            const float top = fmaxf(max3(sr[2 * u][2 * k], sr[2 * u][2 * k + 1],
+                                         sr[2 * u + 1][2 * k]), sr[2 * u + 1][2 * k + 1]);
             mx[k] = u ? fmaxf(mx[k], top * f[u][k]) : top * f[u][k];
           }
-          grows |= mx[k] > m[mt][k] + kSlack || (m[mt][k] == -INFINITY && mx[k] > -INFINITY);
+          grows |= mx[k] > m[k] + kSlack || (m[k] == -INFINITY && mx[k] > -INFINITY);
         }
         if (__any_sync(0xffffffffu, grows)) {
           float a[2];
@@ -458,40 +474,40 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int k = 0; k < 2; ++k) {
             mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
             mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-            const bool up = mx[k] > m[mt][k];  // of the whole row, once any lane of the warp asks
-            a[k] = up ? exp2_fast(m[mt][k] - mx[k]) : 1.f;
-            if (up) m[mt][k] = mx[k];
-            l[mt][k] *= a[k];
+            const bool up = mx[k] > m[k];  // of the whole row, once any lane of the warp asks
+            a[k] = up ? exp2_fast(m[k] - mx[k]) : 1.f;
+            if (up) m[k] = mx[k];
+            l[k] *= a[k];
             a[k] *= grow;
           }
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
-            o[mt][j][0] *= a[0];
-            o[mt][j][1] *= a[0];
-            o[mt][j][2] *= a[1];
-            o[mt][j][3] *= a[1];
+            o[j][0] *= a[0];
+            o[j][1] *= a[0];
+            o[j][2] *= a[1];
+            o[j][3] *= a[1];
           }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float off = kShift - (m[mt][k] == -INFINITY ? 0.f : m[mt][k]);
+          const float off = kShift - (m[k] == -INFINITY ? 0.f : m[k]);
           float sum = 0.f;
 #pragma unroll
           for (int nb = 0; nb < 2 * SUB; ++nb) {
             const float vf = sc[nb / 2].y * vinv;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float e = exp2_fast(fmaf(sr[mt][nb][2 * k + j], f[nb / 2][k], off));
+              const float e = exp2_fast(fmaf(sr[nb][2 * k + j], f[nb / 2][k], off));
               sum += e;
-              sr[mt][nb][2 * k + j] = e * vf;
+              sr[nb][2 * k + j] = e * vf;
             }
           }
-          l[mt][k] += sum;
+          l[k] += sum;
         }
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-          const float(&x)[4] = sr[mt][2 * u], (&y)[4] = sr[mt][2 * u + 1];
-          pa[mt][u] = make_uint4(pack2<__half>(x[0], x[1]), pack2<__half>(x[2], x[3]),
+          const float(&x)[4] = sr[2 * u], (&y)[4] = sr[2 * u + 1];
+          pa[u] = make_uint4(pack2<__half>(x[0], x[1]), pack2<__half>(x[2], x[3]),
                                  pack2<__half>(y[0], y[1]), pack2<__half>(y[2], y[3]));
         }
       }
@@ -533,80 +549,73 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint32_t b1[4] = {e4m3x2_to_f16x2(t23a), e4m3x2_to_f16x2(t23a >> 16),
                                   e4m3x2_to_f16x2(t23b), e4m3x2_to_f16x2(t23b >> 16)};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * j + k], pa[mt][u], b0[k], b1[k]);
+          for (int k = 0; k < 4; ++k) mma16816(o[4 * j + k], pa[u], b0[k], b1[k]);
         }
       }
     }
     if (!ok) break;
 
-    // the next unit's q on its way, the four warps' parts of this one into one: each
-    // writes its own, and all threads add them up
-    Walk nx = w;
-    nx.next(p);
-    if (nx.pos < nx.end) ask_q(nx);
+    // the four warps' parts of the unit into one: each writes its own, and all
+    // threads add them up
     const bool begins = w.tile == 0, ends = w.tile + n == w.tiles;
     float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * L::kRows * (D + kPartStats);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt * 16 >= R) break;
-      if (mt && !(ok = sync())) break;  // the rows before have been read
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 1);
-        l[mt][k] += __shfl_xor_sync(0xffffffffu, l[mt][k], 2);
-        const int r = k * 8 + g;
-        if (mt * 16 + r >= R) continue;
-        if (c == 0) {
-          wm[warp * L::kRows + r] = m[mt][k];
-          wl[warp * L::kRows + r] = l[mt][k];
-        }
-        // piece j / 4 of column block 2c + jj: no two lanes of a store on one bank
-        float* at = buf + warp * (L::kBuf / 4) + r * (D + 4) + 2 * c * 4;
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-          for (int j = 0; j < NB; j += 4)
-            *reinterpret_cast<float4*>(at + (j / 4) * 32 + jj * 4) =
-                make_float4(o[mt][j][2 * k + jj], o[mt][j + 1][2 * k + jj], o[mt][j + 2][2 * k + jj],
-                            o[mt][j + 3][2 * k + jj]);
+    for (int k = 0; k < 2; ++k) {
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+      const int r = k * 8 + g;
+      if (rg * 16 + r >= R) continue;
+      if (c == 0) {
+        wm[warp * 16 + r] = m[k];
+        wl[warp * 16 + r] = l[k];
       }
-      if (lane == 0) wv[warp] = vref;
-      if (!(ok = sync())) break;
-      const float vmax = fmaxf(fmaxf(wv[0], wv[1]), fmaxf(wv[2], wv[3]));
-      const float vdiv = vmax > 0.f ? 1.f / vmax : 0.f;
-      for (int e = threadIdx.x; e < min(16, R - mt * 16) * (D / 4); e += kConsumers) {
-        const int r = e / (D / 4), d4 = e % (D / 4), rr = mt * 16 + r;
-        const float mx = fmaxf(max3(wm[r], wm[L::kRows + r], wm[2 * L::kRows + r]), wm[3 * L::kRows + r]);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
+      // piece j / 4 of column block 2c + jj: no two lanes of a store on one bank
+      float* at = buf + warp * (L::kBuf / 4) + r * (D + 4) + 2 * c * 4;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = exp2_fast(wm[k * L::kRows + r] - ref), b = a * (wv[k] * vdiv);
-          const float4 x = *reinterpret_cast<const float4*>(
-              buf + k * (L::kBuf / 4) + r * (D + 4) + (d4 % (NB / 4)) * 32 + d4 / (NB / 4) * 4);
-          sum += wl[k * L::kRows + r] * a;
-          z = make_float4(z.x + x.x * b, z.y + x.y * b, z.z + x.z * b, z.w + x.w * b);
-        }
-        if (begins && ends) {
-          const int i = rr / p.G, head = w.h * p.G + rr % p.G;
-          const int64_t row = ((int64_t)w.b * p.Hq + head) * p.N + i;
-          const float inv = sum != 0.f ? 1.f / sum : 0.f;
-          uint2 out;
-          out.x = pack2<T>(z.x * inv * vmax, z.y * inv * vmax);
-          out.y = pack2<T>(z.z * inv * vmax, z.w * inv * vmax);
-          *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + row * D + d4 * 4) = out;
-          if (p.lse && d4 == 0) p.lse[row] = (mx - kShift + log2f(sum)) * kLn2;
-        } else {
-          reinterpret_cast<float4*>(part)[rr * (D / 4) + d4] = z;
-          if (d4 == 0)
-            reinterpret_cast<float4*>(part + L::kRows * D)[rr] = make_float4(mx, sum, vmax, 0.f);
-        }
+      for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+        for (int j = 0; j < NB; j += 4)
+          *reinterpret_cast<float4*>(at + (j / 4) * (D / NB * 4) + jj * 4) = make_float4(
+              o[j][2 * k + jj], o[j + 1][2 * k + jj], o[j + 2][2 * k + jj], o[j + 3][2 * k + jj]);
+    }
+    if (lane == 0) wv[warp] = vref;
+    if (!(ok = sync())) break;
+    const float vmax = fmaxf(fmaxf(wv[0], wv[1]), fmaxf(wv[2], wv[3]));
+    const float vdiv = vmax > 0.f ? 1.f / vmax : 0.f;
+    for (int e = threadIdx.x; e < R * (D / 4); e += kConsumers) {
+      const int rr = e / (D / 4), d4 = e % (D / 4), r = rr & 15;
+      const int first = RG == 2 ? (rr >> 4) * 2 : 0;  // of the warps that have this row
+      constexpr int PARTS = 4 / RG;
+      float mx = wm[first * 16 + r];
+#pragma unroll
+      for (int k = 1; k < PARTS; ++k) mx = fmaxf(mx, wm[(first + k) * 16 + r]);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k) {
+        const float a = exp2_fast(wm[(first + k) * 16 + r] - ref), b = a * (wv[first + k] * vdiv);
+        const float4 x = *reinterpret_cast<const float4*>(
+            buf + (first + k) * (L::kBuf / 4) + r * (D + 4) + (d4 % (NB / 4)) * (D / NB * 4) +
+            d4 / (NB / 4) * 4);
+        sum += wl[(first + k) * 16 + r] * a;
+        z = make_float4(z.x + x.x * b, z.y + x.y * b, z.z + x.z * b, z.w + x.w * b);
+      }
+      if (begins && ends) {
+        const int i = rr / p.G, head = w.h * p.G + rr % p.G;
+        const int64_t row = ((int64_t)w.b * p.Hq + head) * p.N + i;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+        uint2 out;
+        out.x = pack2<T>(z.x * inv * vmax, z.y * inv * vmax);
+        out.y = pack2<T>(z.z * inv * vmax, z.w * inv * vmax);
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + row * D + d4 * 4) = out;
+        if (p.lse && d4 == 0) p.lse[row] = (mx - kShift + log2f(sum)) * kLn2;
+      } else {
+        reinterpret_cast<float4*>(part)[rr * (D / 4) + d4] = z;
+        if (d4 == 0)
+          reinterpret_cast<float4*>(part + L::kRows * D)[rr] = make_float4(mx, sum, vmax, 0.f);
       }
     }
-    if (!ok) break;
     if (begins && !ends) {
       // blocks that hold the rest: the share of block k ends at total (k + 1) / shares
       const int64_t unit_end = w.pos + w.tiles;
@@ -615,18 +624,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       while (total * (k + 1) / shares < unit_end) ++k;
       tail = make_int4(k - (int)blockIdx.x, w.b, w.h, 0);
     }
-    w = nx;  // (what this unit left in shared memory is written again after the next sync)
+    w.next(p);  // (what this unit left in shared memory is written again after the next sync)
   }
   if (threadIdx.x == 0) p.tails[blockIdx.x] = ok ? tail : make_int4(0, 0, 0, 0);
   griddep_launch_dependents();
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int RG>
 cudaError_t launch_typed(const AttendParams& p, const CUtensorMap& k, const CUtensorMap& v, int box,
                          int ctas, cudaStream_t stream) {
-  constexpr int bytes = TokenLayout<D, MT>::kBytes;
-  static_assert(bytes <= 113 * 1024, "two blocks for each SM");
-  auto* kernel = token_kernel<T, D, MT>;
+  constexpr int bytes = TokenLayout<D, RG>::kBytes;
+  static_assert(bytes <= (D == 128 ? 113 : 75) * 1024, "two or three blocks for each SM");
+  auto* kernel = token_kernel<T, D, RG>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   kernel<<<ctas, kThreads, bytes, stream>>>(k, v, p, box, kMinTokenTiles);
