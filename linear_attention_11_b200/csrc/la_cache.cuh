@@ -87,14 +87,12 @@ __device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
 }
 
 // ---------------------------------------------------------------- e4m3
-// The two codes in a word's lower half (low byte first) as f16x2, exactly: f16
-// has e4m3's numbers.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-      : "=r"(r)
+// Four codes (low byte first) as two f16x2, exactly: f16 has e4m3's numbers.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(codes));
-  return r;
 }
 
 // Two fp32 numbers as codes, rounded to nearest even (|x| <= 448 here).

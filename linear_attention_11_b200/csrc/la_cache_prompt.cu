@@ -532,8 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           uint32_t y[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            y[2 * k] = hmul2(e4m3x2_to_f16x2(c[k]), f2);
-            y[2 * k + 1] = hmul2(e4m3x2_to_f16x2(c[k] >> 16), f2);
+            uint32_t lo, hi;
+            e4m3x4_to_f16x4(c[k], lo, hi);
+            y[2 * k] = hmul2(lo, f2);
+            y[2 * k + 1] = hmul2(hi, f2);
           }
           st_shared_v4(dst + j * (kRowsPerLoad * 128), y[0], y[1], y[2], y[3]);
           st_shared_v4((dst ^ 16) + j * (kRowsPerLoad * 128), y[4], y[5], y[6], y[7]);

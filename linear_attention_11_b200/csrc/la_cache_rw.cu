@@ -37,7 +37,8 @@ __device__ __forceinline__ void rescale_rows(uint8_t* codes, int rows, float rat
   for (int i = t; i < rows * (D / 4); i += n) {
     uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
     const uint32_t w = *p;
-    const uint32_t a = e4m3x2_to_f16x2(w & 0xffffu), b = e4m3x2_to_f16x2(w >> 16);
+    uint32_t a, b;
+    e4m3x4_to_f16x4(w, a, b);
     const float2 lo = unpack2<__half>(a), hi = unpack2<__half>(b);
     *p = f32x2_to_e4m3x2(lo.x * ratio, lo.y * ratio) |
          (f32x2_to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
@@ -308,8 +309,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p
         float x[8];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float2 lo = unpack2<__half>(e4m3x2_to_f16x2(c[2 * j + k]));
-          const float2 hi = unpack2<__half>(e4m3x2_to_f16x2(c[2 * j + k] >> 16));
+          uint32_t a, b;
+          e4m3x4_to_f16x4(c[2 * j + k], a, b);
+          const float2 lo = unpack2<__half>(a), hi = unpack2<__half>(b);
           x[4 * k] = lo.x * f[i];
           x[4 * k + 1] = lo.y * f[i];
           x[4 * k + 2] = hi.x * f[i];

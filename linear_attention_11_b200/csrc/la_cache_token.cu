@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
           const uint4 a = lds128(sq + ((rg * KS + ks) * 32 + lane) * 16);
 #pragma unroll
           for (int nb = 0; nb < 2 * SUB; ++nb) {
-            const uint32_t k0 = e4m3x2_to_f16x2(kw[nb][ks]), k1 = e4m3x2_to_f16x2(kw[nb][ks] >> 16);
+            uint32_t k0, k1;
+            e4m3x4_to_f16x4(kw[nb][ks], k0, k1);
             mma16816(sr[nb], a, k0, k1);
           }
         }
@@ -540,14 +541,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
         }
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const uint32_t t01a = __byte_perm(vw[0][j], vw[1][j], 0x5140);
-          const uint32_t t01b = __byte_perm(vw[0][j], vw[1][j], 0x7362);
-          const uint32_t t23a = __byte_perm(vw[2][j], vw[3][j], 0x5140);
-          const uint32_t t23b = __byte_perm(vw[2][j], vw[3][j], 0x7362);
-          const uint32_t b0[4] = {e4m3x2_to_f16x2(t01a), e4m3x2_to_f16x2(t01a >> 16),
-                                  e4m3x2_to_f16x2(t01b), e4m3x2_to_f16x2(t01b >> 16)};
-          const uint32_t b1[4] = {e4m3x2_to_f16x2(t23a), e4m3x2_to_f16x2(t23a >> 16),
-                                  e4m3x2_to_f16x2(t23b), e4m3x2_to_f16x2(t23b >> 16)};
+          // two tokens' bytes of a number side by side
+          uint32_t b0[4], b1[4];
+          e4m3x4_to_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x5140), b0[0], b0[1]);
+          e4m3x4_to_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x7362), b0[2], b0[3]);
+          e4m3x4_to_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x5140), b1[0], b1[1]);
+          e4m3x4_to_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x7362), b1[2], b1[3]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma16816(o[4 * j + k], pa[u], b0[k], b1[k]);
         }
