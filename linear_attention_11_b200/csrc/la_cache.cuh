@@ -180,6 +180,31 @@ constexpr float kAttendShift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// n / m for n >= 0, m > 0; in 32 bits where n has them (a 64-bit division takes a
+// few hundred cycles).
+__device__ __forceinline__ int64_t div_short(int64_t n, int64_t m) {
+  return (n | m) >> 32 ? n / m : (int64_t)((uint32_t)n / (uint32_t)m);
+}
+
+// The line of `total` tiles in equal shares for at most `blocks` blocks, of at least
+// two tiles (but the last): block k has [begin(k), begin(k + 1)).
+struct Shares {
+  int64_t each;
+  int n, more;  // shares; how many of them have one more
+  __device__ __forceinline__ Shares(int64_t total, int blocks) {
+    n = (int)min((int64_t)blocks, (total + 1) >> 1);
+    each = n ? div_short(total, n) : 0;
+    more = (int)(total - each * n);
+  }
+  __device__ __forceinline__ int64_t begin(int k) const { return k * each + min(k, more); }
+  // of a unit that ends at `end`: blocks behind block k that hold some of it
+  __device__ __forceinline__ int behind(int k, int64_t end) const {
+    int last = k;
+    while (begin(last + 1) < end) ++last;
+    return last - k;
+  }
+};
+
 // Sum over the block's threads below this one, and over all (kThreads a multiple
 // of 32, scratch for kThreads / 32 numbers).
 template <int kThreads>

@@ -43,7 +43,6 @@ constexpr int kIssue = 16, kPlan = 17;  // the warps that issue products and pla
 constexpr int kPlans = 4;               // units that the plan is ahead at most
 constexpr float kShift = kAttendShift;
 constexpr float kSlack = 8.f;  // growth of a row's maximum that is let pass
-constexpr int kMinTiles = 2;
 // registers of a thread after the split; 640 x 96 at launch
 constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 56;
 static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= 640 * 96, "registers");
@@ -208,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   const int tpt = 128 / p.G;
   Walk w;
   w.tpt = tpt;
-  int64_t total, shares;
+  int64_t total;
+  Shares shares(0, 0);
   {
     int64_t* line = reinterpret_cast<int64_t*>(sm);  // [B] <= kAttendMaxBatch, before any tile
     for (w.b = warp; w.b < p.B; w.b += kThreads / 32) {
@@ -225,18 +225,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += line[b];
     int64_t before = block_exclusive_sum<kThreads>(mine, misc, total);
-    shares = min((int64_t)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+    shares = Shares(total, gridDim.x);
     w.pos = w.end = 0;
-    if ((int64_t)blockIdx.x < shares) {
-      w.pos = total * blockIdx.x / shares;
-      w.end = total * (blockIdx.x + 1) / shares;
+    if ((int)blockIdx.x < shares.n) {
+      w.pos = shares.begin(blockIdx.x);
+      w.end = shares.begin(blockIdx.x + 1);
     }
     if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
       int b = b0;
       for (; w.pos >= before + line[b]; ++b) before += line[b];
       misc[20] = b;
-      misc[21] = (w.pos - before) / (line[b] / p.Hkv);
-      misc[22] = (w.pos - before) % (line[b] / p.Hkv);
+      const int64_t head = div_short(line[b], p.Hkv);  // tiles of a head
+      misc[21] = div_short(w.pos - before, head);
+      misc[22] = w.pos - before - misc[21] * head;
     }
     __syncthreads();
     if (warp == kPlan && w.pos < w.end) {
@@ -289,6 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t st = tmem + lanes + t * 128, ot = tmem + lanes + 256 + t * 128;
     const uint32_t sq = base + t * L::kQ;
+    // a row of 2-byte values: LPR lanes with 16 bytes each, RPI rows at a time
+    constexpr int LPR = D / 8, RPI = 32 / LPR;
+    const int sub = lane / LPR, piece = lane % LPR;
     int it = 0;    // score tiles so far
     int used = 0;  // units in which this row tile had any
     for (int seg = 0;; ++seg) {
@@ -304,42 +308,55 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       const int last = valid ? unit.kv - unit.nq + token : 0x7fffffff;  // last key that the row sees
       if (threadIdx.x == 0 && unit.follow > 0)
         p.tails[blockIdx.x] = make_int4(unit.follow, b, h, qt);
+      const uint32_t rows = __ballot_sync(0xffffffffu, valid);
       release_unit(seg);
       float f = 0.f;
       if (mine > 0) {
         // q: largest entry of the row into [2^14, 2^15), then f16; the sign of the
-        // scale goes here too, so that the scores' factor is not negative
-        // (read twice, the second time from a cache: a whole row would fill the registers)
-        float top = 0.f;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + row * D);
-#pragma unroll 4
-        for (int j = 0; j < D / 8; ++j) {
-          const uint4 x = valid ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        // scale goes here too, so that the scores' factor is not negative.  The warp
+        // reads its 32 rows together, RPI at a time, and hands each row's factor to
+        // the lane that owns it.
+        constexpr int BATCH = 8;
+        float up = 1.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = unpack2<T>(u[k]);
-            top = max3(top, fabsf(v.x), fabsf(v.y));
+        for (int i0 = 0; i0 < LPR; i0 += BATCH) {
+          uint4 x[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int r = (i0 + i) * RPI + sub;
+            const int64_t at = __shfl_sync(0xffffffffu, row, r);
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if ((rows >> r) & 1)
+              x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at * D) + piece);
+          }
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int r = (warp & 3) * 32 + (i0 + i) * RPI + sub;
+            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = unpack2<T>(u[k]);
+              top = max3(top, fabsf(v.x), fabsf(v.y));
+            }
+#pragma unroll
+            for (int k = LPR / 2; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+            const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+            const float f1 = top > 0.f && ex < 128 ? pow2i(max(min(14 - ex, 127), -126)) : 1.f;
+            const float mine1 = __shfl_sync(0xffffffffu, f1, (lane % RPI) * LPR);
+            if (lane / RPI == i0 + i) up = mine1;
+            const float q1 = p.scale < 0.f ? -f1 : f1;
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 y = unpack2<T>(u[k]);
+              v[k] = pack2<__half>(y.x * q1, y.y * q1);
+            }
+            st_shared_v4(sq + (piece >> 3) * (128 * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                         v[0], v[1], v[2], v[3]);
           }
         }
-        const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-        const bool scaled = top > 0.f && ex < 128;
-        const float up = scaled ? pow2i(max(min(14 - ex, 127), -126)) : 1.f;
         f = fabsf(p.scale) * kLog2e / up;
-        const float q1 = p.scale < 0.f ? -up : up;
-#pragma unroll 4
-        for (int j = 0; j < D / 8; ++j) {
-          const uint4 x = valid ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-          uint32_t v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 y = unpack2<T>(u[k]);
-            v[k] = pack2<__half>(y.x * q1, y.y * q1);
-          }
-          st_shared_v4(sq + (j >> 3) * (128 * 128) + rr * 128 + (((j & 7) ^ (rr & 7)) << 4), v[0],
-                       v[1], v[2], v[3]);
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
@@ -429,8 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         tc_fence_after();
       }
       float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * 256 * (D + kPartStats);
+      // Rows go out through the warp's part of the q tile, which its products have
+      // read, so that a store covers whole rows.
       const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
         if (mine > 0) {
@@ -440,9 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = 0u;
         }
-        if (!valid) continue;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + row * D + c * 32);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t y[4];
@@ -450,15 +467,42 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
             for (int j = 0; j < 4; ++j)
               y[j] = pack2<T>(__uint_as_float(x[k * 8 + 2 * j]) * inv * ev,
                               __uint_as_float(x[k * 8 + 2 * j + 1]) * inv * ev);
-            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+            const int pc = c * 4 + k;
+            st_shared_v4(sq + (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4), y[0],
+                         y[1], y[2], y[3]);
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(part + (int64_t)(t * 128 + rr) * D + c * 32);
+          // a part's 32 fp32 columns: eight lanes a row
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            dst[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            st_shared_v4(sq + rr * 128 + ((k ^ (rr & 7)) << 4), x[4 * k], x[4 * k + 1], x[4 * k + 2],
+                         x[4 * k + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r1 = i * 4 + (lane >> 3), r = (warp & 3) * 32 + r1, k = lane & 7;
+            uint4 y;
+            ld_shared_v4(sq + r * 128 + ((k ^ (r & 7)) << 4), y.x, y.y, y.z, y.w);
+            if ((rows >> r1) & 1)
+              *reinterpret_cast<uint4*>(part + (int64_t)(t * 128 + r) * D + c * 32 + k * 4) = y;
+          }
         }
       }
+      if (whole) {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < LPR; ++i) {
+          const int r1 = i * RPI + sub, r = (warp & 3) * 32 + r1;
+          const int64_t at = __shfl_sync(0xffffffffu, row, r1);
+          uint4 y;
+          ld_shared_v4(sq + (piece >> 3) * (128 * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4), y.x, y.y,
+                       y.z, y.w);
+          if ((rows >> r1) & 1)
+            *(reinterpret_cast<uint4*>(static_cast<T*>(p.o) + at * D) + piece) = y;
+        }
+      }
+      __syncwarp();
       tc_fence_before();
       if (valid && whole) {
         if (p.lse) p.lse[row] = (m - kShift + log2f(l)) * kLn2;
@@ -696,13 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
             unit.nq = w.nq;
             unit.begins = w.tile == 0;
             unit.ends = w.tile + n == w.tiles;
-            unit.follow = 0;
-            if (unit.begins && !unit.ends) {
-              // the share of block k ends at total (k + 1) / shares
-              int k = blockIdx.x;
-              while (total * (k + 1) / shares < w.pos + w.tiles) ++k;
-              unit.follow = k - (int)blockIdx.x;
-            }
+            unit.follow =
+                unit.begins && !unit.ends ? shares.behind(blockIdx.x, w.pos + w.tiles) : 0;
             unit.ek = ek;
             unit.ev = ev;
           }

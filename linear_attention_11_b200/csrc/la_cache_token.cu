@@ -44,7 +44,6 @@ constexpr int kConsumers = 128;  // four warps
 constexpr int kThreads = kConsumers + 32;
 constexpr float kShift = kAttendShift;
 constexpr float kSlack = 8.f;   // growth of a row's maximum that is let pass
-constexpr int kMinTokenTiles = 2;
 
 // RG row groups of 16 rows: with one, two warps take a stage's 64 tokens, 32 each,
 // and the other two the next stage's; with two, all four take every stage, two for each
@@ -142,8 +141,7 @@ struct Walk {
 template <typename T, int D, int RG>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     token_kernel(const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const AttendParams p, int box,
-                 int min_tiles) {
+                 const __grid_constant__ CUtensorMap map_v, const AttendParams p, int box) {
   using L = TokenLayout<D, RG>;
   constexpr int KS = D / 16;  // 16-wide steps of q . k
   constexpr int NB = D / 8;   // 8-wide blocks of the output
@@ -183,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
   // The line's length, this block's share of it, and the unit where that begins.
   Walk w;
   int64_t total;
+  Shares shares(0, 0);
   {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
@@ -192,11 +191,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       mine += (int64_t)w.tiles * p.Hkv;
     }
     int64_t before = block_exclusive_sum<kThreads>(mine, misc, total);
-    const int64_t shares = min((int64_t)gridDim.x, (total + min_tiles - 1) / min_tiles);
+    shares = Shares(total, gridDim.x);
     w.pos = w.end = 0;
-    if ((int64_t)blockIdx.x < shares) {
-      w.pos = total * blockIdx.x / shares;
-      w.end = total * (blockIdx.x + 1) / shares;
+    if ((int)blockIdx.x < shares.n) {
+      w.pos = shares.begin(blockIdx.x);
+      w.end = shares.begin(blockIdx.x + 1);
     }
     if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
       for (w.b = b0;; ++w.b) {
@@ -205,8 +204,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
         before += (int64_t)w.tiles * p.Hkv;
       }
       misc[6] = w.b;
-      misc[7] = (w.pos - before) / w.tiles;
-      misc[8] = (w.pos - before) % w.tiles;
+      misc[7] = div_short(w.pos - before, w.tiles);
+      misc[8] = w.pos - before - misc[7] * w.tiles;
     }
     __syncthreads();
     if (w.pos >= w.end) {
@@ -616,12 +615,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       }
     }
     if (begins && !ends) {
-      // blocks that hold the rest: the share of block k ends at total (k + 1) / shares
-      const int64_t unit_end = w.pos + w.tiles;
-      const int64_t shares = min((int64_t)gridDim.x, (total + min_tiles - 1) / min_tiles);
-      int k = blockIdx.x;
-      while (total * (k + 1) / shares < unit_end) ++k;
-      tail = make_int4(k - (int)blockIdx.x, w.b, w.h, 0);
+      tail = make_int4(shares.behind(blockIdx.x, w.pos + w.tiles), w.b, w.h, 0);
     }
     w.next(p);  // (what this unit left in shared memory is written again after the next sync)
   }
@@ -637,7 +631,7 @@ cudaError_t launch_typed(const AttendParams& p, const CUtensorMap& k, const CUte
   auto* kernel = token_kernel<T, D, RG>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kThreads, bytes, stream>>>(k, v, p, box, kMinTokenTiles);
+  kernel<<<ctas, kThreads, bytes, stream>>>(k, v, p, box);
   return cudaGetLastError();
 }
 
