@@ -67,7 +67,7 @@ struct PromptLayout {
   static constexpr int kMiscOff = kSlotOff + kSlots * kSlot;
   static constexpr int kUnitOff = kMiscOff + 23 * 8;  // scan scratch 20 x 8, start 3 x 8
   static constexpr int kBarOff = kUnitOff + kPlans * 64;
-  static constexpr int kBars = 2 * kSlots + 2 * 4 + 2 * kPlans + 1;
+  static constexpr int kBars = 2 * kSlots + 2 * 5 + 2 * kPlans + 1;
   static constexpr int kEnd = kBarOff + kBars * 8 + 16;  // tmem slot, abort flag
   static constexpr int kBytes = kEnd + 1024;
 };
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   uint64_t* q_full = kv_empty + L::kSlots;  // [2] a unit's q tile is in shared memory
   uint64_t* s_full = q_full + 2;            // [2] a score tile is computed
   uint64_t* p_full = s_full + 2;            // [2] its weights are written, O is rescaled
-  uint64_t* o_full = p_full + 2;            // [2] a unit's last product with V is added
+  uint64_t* o_full = p_full + 4;            // [2] a unit's last product with V is added
   uint64_t* u_full = o_full + 2;            // [kPlans] a unit is written down
   uint64_t* u_empty = u_full + kPlans;      // [kPlans] every role has read it
   uint64_t* done = u_empty + kPlans;
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 4);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[2 * t], 4);
+      mbar_init(&p_full[2 * t + 1], 4);
       mbar_init(&o_full[t], 1);
     }
     for (int k = 0; k < kPlans; ++k) {
@@ -428,13 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
             y[k] = pack2<__half>(w.x, w.y);
           }
           tmem_st32(st + half * 32, y);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
         }
         sum = add2(sum, sum2);
         l = sum.x + sum.y;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
 
@@ -572,14 +573,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         for (int j = 0; j < kLoads; ++j) {
           const uint32_t fj = __shfl_sync(0xffffffffu, fw, (j * kRowsPerLoad + sub) >> 4);
           const __half2 f2 = *reinterpret_cast<const __half2*>(&fj);
+          const bool one = fj == 0x3c003c00u;  // as for most pages: no product needed
           const uint32_t c[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
           uint32_t y[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t lo, hi;
             e4m3x4_to_f16x4(c[k], lo, hi);
-            y[2 * k] = hmul2(lo, f2);
-            y[2 * k + 1] = hmul2(hi, f2);
+            y[2 * k] = lo;
+            y[2 * k + 1] = hi;
+          }
+          if (!one) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = hmul2(y[k], f2);
           }
           st_shared_v4(dst + j * (kRowsPerLoad * 128), y[0], y[1], y[2], y[3]);
           st_shared_v4((dst ^ 16) + j * (kRowsPerLoad * 128), y[4], y[5], y[6], y[7]);
@@ -672,15 +678,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         for (int t = 0; t < 2; ++t) {
           const int c = t ? c1 : c0;
           if (i >= c) continue;
-          ok = mbar_wait_brief(&p_full[t], (p_parity >> t) & 1, abort_flag);
-          if (!ok) break;
-          p_parity ^= 1u << t;
-          tc_fence_after();
           const uint32_t pt = tmem + t * 128;
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)  // O += P V
-            mma_ts(pt + 256, pt + kk * 8, smem_desc_sw128(vt + kk * 2048, kKeys * 128, 1024),
-                   IDESC_PV, i > 0 || kk > 0 ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            ok = mbar_wait_brief(&p_full[2 * t + h], (p_parity >> t) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)  // O += P V
+              mma_ts(pt + 256, pt + kk * 8, smem_desc_sw128(vt + kk * 2048, kKeys * 128, 1024),
+                     IDESC_PV, i > 0 || kk > 0 ? 1u : 0u);
+          }
+          if (!ok) break;
+          p_parity ^= 1u << t;
           if (i + 1 < c) scores(t, kt);
           else mma_commit(&o_full[t]);
         }

@@ -28,8 +28,7 @@ class Bar:
 
 
 class Model:
-    """units: for each unit of a block's share the score tiles (of 64 keys) of row tile 0 and of row
-    tile 1; two of them to a key tile, which is what is converted."""
+    """units: for each unit of a block's share the key tiles that row tile 0 and row tile 1 see."""
 
     PLANS = 4
 
@@ -38,14 +37,14 @@ class Model:
         self.rng = random.Random(seed)
         some = lambda n, k, c: [Bar(f"{n}[{t}]", c) for t in range(k)]  # noqa: E731
         self.kv_full, self.kv_empty = some("kv_full", slots, 8), some("kv_empty", slots, 1)
-        self.q_full, self.o_full = some("q", 2, 4), some("o", 4, 1)
-        self.s_full, self.p_full = some("s", 4, 1), some("p", 4, 4)
+        self.q_full, self.s_full, self.o_full = some("q", 2, 4), some("s", 2, 1), some("o", 2, 1)
+        self.p_full = some("p", 4, 4)                     # for each row tile its two halves
         self.u_full, self.u_empty = some("u_full", self.PLANS, 1), some("u_empty", self.PLANS, 17)
         self.queue = []                                   # products and commits in issue order
         self.slot = [[None] * 8 for _ in range(slots)]    # what each converting warp wrote
         self.q = [[None] * 4 for _ in range(2)]
         self.p = [[None] * 4 for _ in range(4)]
-        self.s, self.o = [None] * 4, [None] * 2
+        self.s, self.o = [None] * 2, [None] * 2
         self.plan = [None] * self.PLANS
         self.stored = set()
 
@@ -74,7 +73,7 @@ class Model:
             yield self.u_full[k].arrive
 
     def softmax(self, t, w):
-        it = 0
+        it = used = 0
         for seg, c in enumerate(self.units):
             yield from self.unit(seg)
             if c[t]:
@@ -82,34 +81,29 @@ class Model:
                 self.q[t][w] = seg
                 yield self.q_full[t].arrive
             for i in range(c[t]):
-                buf = 2 * t + (0 if self.mistake == "one barrier for both buffers" else it & 1)
-                yield self.s_full[buf], it if self.mistake == "one barrier for both buffers" else it >> 1
-                self.expect(self.s[2 * t + (it & 1)], (seg, i), f"scores {t}")
+                yield self.s_full[t], it
+                self.expect(self.s[t], (seg, i), f"scores {t}")
                 if i and self.rng.random() < 0.3:          # the maximum grows: O is rescaled
-                    if self.mistake != "no wait to rescale":
-                        yield self.product(t, it - 1)
                     self.expect(self.o[t], (seg, i - 1), f"O {t} to rescale")
-                self.p[2 * t + (it & 1)][w] = (seg, i)
-                yield self.p_full[buf].arrive
+                for h in range(2):
+                    self.expect(self.s[t], (seg, i), f"scores {t}, half {h}")
+                    self.p[2 * t + h][w] = (seg, i)
+                    yield self.p_full[2 * t + (0 if self.mistake == "one barrier for both halves" else h)].arrive
                 it += 1
             if c[t]:
                 if self.mistake != "no wait for the output":
-                    yield self.product(t, it - 1)
+                    yield self.o_full[t], used
+                used += 1
                 self.expect(self.o[t], (seg, c[t] - 1), f"output {t}")
+                self.unread(("q", t))                      # rows go out through the q tile
             self.stored.add((seg, t, w))
         yield from self.unit(len(self.units))
-
-    def product(self, t, i):
-        """The barrier and phase of the product of score tile i with V."""
-        if self.mistake == "one barrier for all products":
-            return self.o_full[t], i
-        return self.o_full[2 * t + (i & 1)], i >> 1
 
     def convert(self, w):
         u = 0
         for seg, c in enumerate(self.units):
             yield from self.unit(seg)
-            for i in range((max(c) + 1) // 2):
+            for i in range(max(c)):
                 for kind in "kv":
                     s = u % self.slots
                     if u >= self.slots and self.mistake != "no wait for a slot":
@@ -120,61 +114,64 @@ class Model:
                     u += 1
         yield from self.unit(len(self.units))
 
-    def scores(self, t, u, seg, j, buf):
-        s = u % self.slots
-
+    def scores(self, t, s, seg, i):
         def run():
-            self.expect(self.slot[s], [(seg, j // 2, "k")] * 8, f"slot {s}")
+            self.expect(self.slot[s], [(seg, i, "k")] * 8, f"slot {s}")
             self.expect(self.q[t], [seg] * 4, f"q {t}")
-            if j >= 2:
-                self.expect(self.p[buf], [(seg, j - 2)] * 4, f"weights {t} before new scores")
-                if self.o[t] is None or self.o[t] < (seg, j - 2):
-                    raise Fault("scores over weights that have not met V")
-            self.s[buf] = (seg, j)
-        self.queue += [((("slot", s), ("q", t)), run), ((), self.s_full[self.bar(buf)].arrive)]
-
-    def bar(self, buf):
-        return buf & ~1 if self.mistake == "one barrier for both buffers" else buf
+            if i:
+                self.expect(self.o[t], (seg, i - 1), f"weights {t} under new scores have met V")
+            self.s[t] = (seg, i)
+        self.queue += [((("slot", s), ("q", t)), run), ((), self.s_full[t].arrive)]
 
     def issue(self):
-        u, it, units = 0, [0, 0], [0, 0]
+        u, tiles, units = 0, [0, 0], [0, 0]
         commit = lambda b: self.queue.append(((), b.arrive))  # noqa: E731
         full = lambda k: (self.kv_full[k % self.slots], k // self.slots)  # noqa: E731
         for seg, c in enumerate(self.units):
             yield from self.unit(seg)
             n = max(c)
-            for j in range(-2, n) if n else ():
-                for t in range(2):
-                    i = it[t] + j
-                    buf = 2 * t + (i & 1)
-                    if j == -2 and c[t]:
+            if not n:
+                continue
+            yield full(u)
+            for t in range(2):
+                if c[t]:
+                    if self.mistake != "no wait for q":
                         yield self.q_full[t], units[t]
-                        units[t] += 1
-                    if 0 <= j < c[t]:
-                        if self.mistake != "no wait for weights":
-                            yield self.p_full[self.bar(buf)], \
-                                i if self.mistake == "one barrier for both buffers" else i >> 1
-                        v = u + (j & ~1) + 1
-                        yield full(v)
+                    units[t] += 1
+                    self.scores(t, u % self.slots, seg, 0)
+            commit(self.kv_empty[u % self.slots])
+            u += 1
+            for i in range(n):
+                v, u = u, u + 1
+                yield full(v)
+                if i + 1 < n:
+                    yield full(u)
+                for t in range(2):
+                    if i >= c[t]:
+                        continue
+                    for h in range(2):
+                        if self.mistake == "one barrier for both halves":
+                            yield self.p_full[2 * t], 2 * tiles[t] + h
+                        elif self.mistake != "no wait for weights":
+                            yield self.p_full[2 * t + h], tiles[t]
 
-                        def run(t=t, j=j, seg=seg, buf=buf, s=v % self.slots):
-                            self.expect(self.slot[s], [(seg, j // 2, "v")] * 8, f"slot {s}")
-                            self.expect(self.p[buf], [(seg, j)] * 4, f"weights {t}")
-                            if j:
-                                self.expect(self.o[t], (seg, j - 1), f"O {t}")
-                            self.o[t] = (seg, j)
+                        def run(t=t, i=i, h=h, seg=seg, s=v % self.slots):
+                            self.expect(self.slot[s], [(seg, i, "v")] * 8, f"slot {s}")
+                            self.expect(self.p[2 * t + h], [(seg, i)] * 4, f"weights {t}")
+                            if h:
+                                self.o[t] = (seg, i)
+                            elif i:
+                                self.expect(self.o[t], (seg, i - 1), f"O {t}")
                         self.queue.append(((("slot", v % self.slots),), run))
-                        commit(self.product(t, i)[0])
-                    if j + 2 < c[t]:
-                        k = u + ((j + 2) & ~1)
-                        yield full(k)
-                        self.scores(t, k, seg, j + 2, buf)
-                if j >= 0 and (j & 1 or j == n - 1):
-                    commit(self.kv_empty[(u + (j & ~1) + 1) % self.slots])
-                if j + 2 < n and (j & 1 or j + 2 == n - 1):
-                    commit(self.kv_empty[(u + ((j + 2) & ~1)) % self.slots])
-            u += (n + 1) & ~1
-            it = [it[0] + c[0], it[1] + c[1]]
+                    tiles[t] += 1
+                    if i + 1 < c[t]:
+                        self.scores(t, u % self.slots, seg, i + 1)
+                    else:
+                        commit(self.o_full[t])
+                commit(self.kv_empty[v % self.slots])
+                if i + 1 < n:
+                    commit(self.kv_empty[u % self.slots])
+                    u += 1
         yield from self.unit(len(self.units))
 
     def run(self):
@@ -222,9 +219,8 @@ def test_protocol(slots):
         Model(units_of(rng), slots, seed).run()
 
 
-@pytest.mark.parametrize("mistake", ["no wait for the readers of a plan", "no wait to rescale",
-                                     "one barrier for both buffers", "one barrier for all products",
-                                     "no wait for the output",
+@pytest.mark.parametrize("mistake", ["no wait for the readers of a plan", "no wait for q",
+                                     "one barrier for both halves", "no wait for the output",
                                      "no wait for a slot", "no wait for weights"])
 def test_planted_protocol_mistakes(mistake):
     rng, caught = random.Random(1), 0
