@@ -7,6 +7,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "la_internal.h"
 
 namespace la {
@@ -17,11 +19,25 @@ constexpr unsigned kDevNonfinite = 0x4u;  // LA_DEV_NONFINITE
 struct AttendParams;
 struct JoinGeometry;
 cudaError_t launch_cache_token(const AttendParams& p, const la_cache& c, la_dtype dtype, int rows,
-                               int ctas, cudaStream_t stream);
+                               int ctas, bool whole, cudaStream_t stream);
 cudaError_t launch_cache_prompt(const AttendParams& p, la_dtype dtype, int d, int ctas,
                                 cudaStream_t stream);
 cudaError_t launch_cache_join(const AttendParams& p, const JoinGeometry& g, la_dtype dtype, int d,
                               int ctas, cudaStream_t stream);
+
+// Lets a kernel use `bytes` of shared memory on the current device, once for each.
+template <auto kKernel>
+cudaError_t allow_shared(int bytes) {
+  static std::atomic<uint64_t> done{0};  // bit for each device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 inline int page_log2(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
@@ -187,12 +203,12 @@ __device__ __forceinline__ int64_t div_short(int64_t n, int64_t m) {
 }
 
 // The line of `total` tiles in equal shares for at most `blocks` blocks, of at least
-// two tiles (but the last): block k has [begin(k), begin(k + 1)).
+// `least` (1 or 2) tiles: block k has [begin(k), begin(k + 1)).
 struct Shares {
   int64_t each;
   int n, more;  // shares; how many of them have one more
-  __device__ __forceinline__ Shares(int64_t total, int blocks) {
-    n = (int)min((int64_t)blocks, (total + 1) >> 1);
+  __device__ __forceinline__ Shares(int64_t total, int blocks, int least) {
+    n = (int)min((int64_t)blocks, (total + least - 1) >> (least - 1));
     each = n ? div_short(total, n) : 0;
     more = (int)(total - each * n);
   }

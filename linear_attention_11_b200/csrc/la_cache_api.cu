@@ -106,6 +106,18 @@ la_status check_attend(const void* q, la_dtype dtype, const la_cache* c, const i
 
 la_status from_cuda(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
 
+// An attention call with its arguments checked.
+la_status run_attend(const void* q, la_dtype dtype, const la_cache* c, const int32_t* table,
+                     const int32_t* kv_len, const int32_t* q_len, void* o, float* lse, int B,
+                     int Hq, int64_t N, int max_pages, float scale, void* workspace,
+                     cudaStream_t stream) {
+  unsigned* status = device_status_ptr();
+  const int sms = device_sms();
+  if (!status || sms <= 0) return LA_ERR_CUDA;
+  return from_cuda(launch_cache_attend(*c, q, dtype, table, kv_len, q_len, o, lse, B, Hq, N,
+                                       max_pages, scale, workspace, status, sms, stream));
+}
+
 }  // namespace
 }  // namespace la
 
@@ -152,10 +164,8 @@ LA_EXPORT la_status la_cache_attend_ws(const void* q, la_dtype dtype, const la_c
   const la_status st = check_attend(q, dtype, cache, table, kv_len, q_len, o, lse, B, Hq, N,
                                     max_pages, scale);
   if (st != LA_OK) return st;
-  unsigned* status = device_status_ptr();
-  const int sms = device_sms();
-  if (!status || sms <= 0) return LA_ERR_CUDA;
-  const size_t need = attend_workspace_bytes(B, Hq, cache->Hkv, N, cache->d, sms);
+  const size_t need = la_cache_attend_workspace_bytes(B, Hq, cache->Hkv, N, cache->d);
+  if (need == 0) return LA_ERR_CUDA;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return LA_ERR_WORKSPACE;
   Range r[4];
   cache_ranges(cache, r);
@@ -164,9 +174,8 @@ LA_EXPORT la_status la_cache_attend_ws(const void* q, la_dtype dtype, const la_c
   if (any_meets(w, r, 4) || meets(w, {q, rows * cache->d * 2}) ||
       meets(w, {o, rows * cache->d * 2}) || meets(w, {lse, rows * 4}))
     return LA_ERR_WORKSPACE;
-  return from_cuda(launch_cache_attend(*cache, q, dtype, table, kv_len, q_len, o, lse, B, Hq, N,
-                                       max_pages, scale, workspace, status, sms,
-                                       static_cast<cudaStream_t>(stream)));
+  return run_attend(q, dtype, cache, table, kv_len, q_len, o, lse, B, Hq, N, max_pages, scale,
+                    workspace, static_cast<cudaStream_t>(stream));
 }
 
 LA_EXPORT la_status la_cache_attend(const void* q, la_dtype dtype, const la_cache* cache,
@@ -176,13 +185,15 @@ LA_EXPORT la_status la_cache_attend(const void* q, la_dtype dtype, const la_cach
   la_status st = check_attend(q, dtype, cache, table, kv_len, q_len, o, lse, B, Hq, N, max_pages,
                               scale);
   if (st != LA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!attend_uses_workspace(Hq / cache->Hkv, N, (int64_t)max_pages * cache->page))
+    return run_attend(q, dtype, cache, table, kv_len, q_len, o, lse, B, Hq, N, max_pages, scale,
+                      nullptr, s);
   const size_t bytes = la_cache_attend_workspace_bytes(B, Hq, cache->Hkv, N, cache->d);
   if (bytes == 0 || !keep_pool_memory()) return LA_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* ws = nullptr;
   if (cudaMallocAsync(&ws, bytes, s) != cudaSuccess) return LA_ERR_CUDA;
-  st = la_cache_attend_ws(q, dtype, cache, table, kv_len, q_len, o, lse, B, Hq, N, max_pages,
-                          scale, ws, bytes, stream);
+  st = run_attend(q, dtype, cache, table, kv_len, q_len, o, lse, B, Hq, N, max_pages, scale, ws, s);
   if (cudaFreeAsync(ws, s) != cudaSuccess && st == LA_OK) st = LA_ERR_CUDA;
   return st;
 }

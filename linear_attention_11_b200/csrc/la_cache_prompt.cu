@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   Walk w;
   w.tpt = tpt;
   int64_t total;
-  Shares shares(0, 0);
+  Shares shares(0, 0, 1);
   {
     int64_t* line = reinterpret_cast<int64_t*>(sm);  // [B] <= kAttendMaxBatch, before any tile
     for (w.b = warp; w.b < p.B; w.b += kThreads / 32) {
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += line[b];
     int64_t before = block_exclusive_sum<kThreads>(mine, misc, total);
-    shares = Shares(total, gridDim.x);
+    shares = Shares(total, gridDim.x, 2);
     w.pos = w.end = 0;
     if ((int)blockIdx.x < shares.n) {
       w.pos = shares.begin(blockIdx.x);
@@ -778,10 +778,9 @@ template <typename T, int D>
 cudaError_t launch_typed(const AttendParams& p, int ctas, cudaStream_t stream) {
   constexpr int bytes = PromptLayout<D>::kBytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
-  auto* kernel = prompt_kernel<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_shared<prompt_kernel<T, D>>(bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kThreads, bytes, stream>>>(p);
+  prompt_kernel<T, D><<<ctas, kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -114,6 +114,7 @@ struct Walk {
   int tile;          // its place in the unit
   int tiles;         // tiles of the unit (0: sequence without work)
   int kv, nq;        // its lengths
+  bool whole;        // units are not cut: each is one step of the line
 
   __device__ void load(const AttendParams& p) {
     const int64_t len = p.kv_len[b], n = p.q_len ? (int64_t)p.q_len[b] : p.N;
@@ -122,11 +123,15 @@ struct Walk {
     nq = (int)n;
     tiles = ok && n > 0 ? max(1, (int)((len + kTile - 1) / kTile)) : 0;
   }
+  // the length of the line that a unit of this sequence takes
+  __device__ int length() const { return whole ? min(tiles, 1) : tiles; }
   // the unit's tiles in this share: from `tile`, as many as returned
-  __device__ int count() const { return (int)min((int64_t)(tiles - tile), end - pos); }
+  __device__ int count() const {
+    return whole ? tiles : (int)min((int64_t)(tiles - tile), end - pos);
+  }
   // on to the next unit that has tiles (the share goes on)
   __device__ void next(const AttendParams& p) {
-    pos += tiles - tile;
+    pos += length() - tile;
     tile = 0;
     if (++h < p.Hkv) return;
     h = 0;
@@ -141,7 +146,7 @@ struct Walk {
 template <typename T, int D, int RG>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     token_kernel(const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const AttendParams p, int box) {
+                 const __grid_constant__ CUtensorMap map_v, const AttendParams p, int box, bool whole) {
   using L = TokenLayout<D, RG>;
   constexpr int KS = D / 16;  // 16-wide steps of q . k
   constexpr int NB = D / 8;   // 8-wide blocks of the output
@@ -181,17 +186,18 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
   // The line's length, this block's share of it, and the unit where that begins.
   Walk w;
   int64_t total;
-  Shares shares(0, 0);
+  Shares shares(0, 0, 1);
+  w.whole = whole;
   {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
     int64_t mine = 0;
     for (w.b = b0; w.b < b1; ++w.b) {
       w.load(p);
-      mine += (int64_t)w.tiles * p.Hkv;
+      mine += (int64_t)w.length() * p.Hkv;
     }
     int64_t before = block_exclusive_sum<kThreads>(mine, misc, total);
-    shares = Shares(total, gridDim.x);
+    shares = Shares(total, gridDim.x, whole ? 1 : 2);
     w.pos = w.end = 0;
     if ((int)blockIdx.x < shares.n) {
       w.pos = shares.begin(blockIdx.x);
@@ -200,16 +206,16 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
       for (w.b = b0;; ++w.b) {
         w.load(p);
-        if (w.pos < before + (int64_t)w.tiles * p.Hkv) break;
-        before += (int64_t)w.tiles * p.Hkv;
+        if (w.pos < before + (int64_t)w.length() * p.Hkv) break;
+        before += (int64_t)w.length() * p.Hkv;
       }
       misc[6] = w.b;
-      misc[7] = div_short(w.pos - before, w.tiles);
-      misc[8] = w.pos - before - misc[7] * w.tiles;
+      misc[7] = div_short(w.pos - before, w.length());
+      misc[8] = w.pos - before - misc[7] * w.length();
     }
     __syncthreads();
     if (w.pos >= w.end) {
-      if (threadIdx.x == 0) p.tails[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (threadIdx.x == 0 && !whole) p.tails[blockIdx.x] = make_int4(0, 0, 0, 0);
       griddep_launch_dependents();
       return;
     }
@@ -619,43 +625,42 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     }
     w.next(p);  // (what this unit left in shared memory is written again after the next sync)
   }
-  if (threadIdx.x == 0) p.tails[blockIdx.x] = ok ? tail : make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0 && !whole) p.tails[blockIdx.x] = ok ? tail : make_int4(0, 0, 0, 0);
   griddep_launch_dependents();
 }
 
 template <typename T, int D, int RG>
 cudaError_t launch_typed(const AttendParams& p, const CUtensorMap& k, const CUtensorMap& v, int box,
-                         int ctas, cudaStream_t stream) {
+                         int ctas, bool whole, cudaStream_t stream) {
   constexpr int bytes = TokenLayout<D, RG>::kBytes;
   static_assert(bytes <= (D == 128 ? 113 : 75) * 1024, "two or three blocks for each SM");
-  auto* kernel = token_kernel<T, D, RG>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_shared<token_kernel<T, D, RG>>(bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kThreads, bytes, stream>>>(k, v, p, box);
+  token_kernel<T, D, RG><<<ctas, kThreads, bytes, stream>>>(k, v, p, box, whole);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_rows(const AttendParams& p, const CUtensorMap& k, const CUtensorMap& v, int box,
-                        int rows, int ctas, cudaStream_t stream) {
-  return rows <= 16 ? launch_typed<T, D, 1>(p, k, v, box, ctas, stream)
-                    : launch_typed<T, D, 2>(p, k, v, box, ctas, stream);
+                        int rows, int ctas, bool whole, cudaStream_t stream) {
+  return rows <= 16 ? launch_typed<T, D, 1>(p, k, v, box, ctas, whole, stream)
+                    : launch_typed<T, D, 2>(p, k, v, box, ctas, whole, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_token(const AttendParams& p, const la_cache& c, la_dtype dtype, int rows,
-                               int ctas, cudaStream_t stream) {
+                               int ctas, bool whole, cudaStream_t stream) {
   CUtensorMap k, v;
   const int box = std::min(c.page, kTile);
   if (!make_tmap_codes(&k, c.k_codes, c.num_pages * c.Hkv * c.page, c.d, box) ||
       !make_tmap_codes(&v, c.v_codes, c.num_pages * c.Hkv * c.page, c.d, box))
     return cudaErrorInvalidValue;
   if (c.d == 64)
-    return dtype == LA_BF16 ? launch_rows<__nv_bfloat16, 64>(p, k, v, box, rows, ctas, stream)
-                            : launch_rows<__half, 64>(p, k, v, box, rows, ctas, stream);
-  return dtype == LA_BF16 ? launch_rows<__nv_bfloat16, 128>(p, k, v, box, rows, ctas, stream)
-                          : launch_rows<__half, 128>(p, k, v, box, rows, ctas, stream);
+    return dtype == LA_BF16 ? launch_rows<__nv_bfloat16, 64>(p, k, v, box, rows, ctas, whole, stream)
+                            : launch_rows<__half, 64>(p, k, v, box, rows, ctas, whole, stream);
+  return dtype == LA_BF16 ? launch_rows<__nv_bfloat16, 128>(p, k, v, box, rows, ctas, whole, stream)
+                          : launch_rows<__half, 128>(p, k, v, box, rows, ctas, whole, stream);
 }
 
 }  // namespace la
