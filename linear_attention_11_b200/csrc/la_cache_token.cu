@@ -70,23 +70,11 @@ struct TokenLayout {
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  ld_shared_v4(addr, v.x, v.y, v.z, v.w);
-  return v;
-}
-
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint64_t* bar, int c0,
@@ -313,6 +301,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
   // -------------------------------------------------------------- products
   const int g = lane >> 2, c = lane & 3, rg = RG == 2 ? warp >> 1 : 0;
   const uint32_t sq = base + L::kQOff;
+  // plain loads: the compiler places them, behind the waits that order them
+  auto lds128 = [&](uint32_t addr) { return *reinterpret_cast<const uint4*>(sm + (addr - base)); };
+  auto lds64 = [&](uint32_t addr) { return *reinterpret_cast<const uint2*>(sm + (addr - base)); };
   int it = 0, syncs = 0;
   auto sync = [&]() { return warps_sync(consumers, syncs, p.status, abort_flag); };
   int4 tail = make_int4(0, 0, 0, 0);
