@@ -20,7 +20,7 @@ struct AttendParams;
 struct JoinGeometry;
 cudaError_t launch_cache_token(const AttendParams& p, const la_cache& c, la_dtype dtype, int rows,
                                int ctas, bool whole, cudaStream_t stream);
-cudaError_t launch_cache_prompt(const AttendParams& p, la_dtype dtype, int d, int ctas,
+cudaError_t launch_cache_prompt(const AttendParams& p, la_dtype dtype, int d, int ctas, bool whole,
                                 cudaStream_t stream);
 cudaError_t launch_cache_join(const AttendParams& p, const JoinGeometry& g, la_dtype dtype, int d,
                               int ctas, cudaStream_t stream);
@@ -202,13 +202,13 @@ __device__ __forceinline__ int64_t div_short(int64_t n, int64_t m) {
   return (n | m) >> 32 ? n / m : (int64_t)((uint32_t)n / (uint32_t)m);
 }
 
-// The line of `total` tiles in equal shares for at most `blocks` blocks, of at least
-// `least` (1 or 2) tiles: block k has [begin(k), begin(k + 1)).
+// The line of `total` tiles in equal shares for at most `blocks` blocks, of two tiles
+// or more: block k has [begin(k), begin(k + 1)).
 struct Shares {
   int64_t each;
   int n, more;  // shares; how many of them have one more
-  __device__ __forceinline__ Shares(int64_t total, int blocks, int least) {
-    n = (int)min((int64_t)blocks, (total + least - 1) >> (least - 1));
+  __device__ __forceinline__ Shares(int64_t total, int blocks) {
+    n = (int)min((int64_t)blocks, (total + 1) >> 1);
     each = n ? div_short(total, n) : 0;
     more = (int)(total - each * n);
   }

@@ -186,7 +186,10 @@ LA_EXPORT la_status la_cache_attend(const void* q, la_dtype dtype, const la_cach
                               scale);
   if (st != LA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!attend_uses_workspace(Hq / cache->Hkv, N, (int64_t)max_pages * cache->page))
+  const int sms = device_sms();
+  if (sms <= 0) return LA_ERR_CUDA;
+  if (!attend_uses_workspace(B, cache->Hkv, Hq / cache->Hkv, N, cache->d,
+                             (int64_t)max_pages * cache->page, sms))
     return run_attend(q, dtype, cache, table, kv_len, q_len, o, lse, B, Hq, N, max_pages, scale,
                       nullptr, s);
   const size_t bytes = la_cache_attend_workspace_bytes(B, Hq, cache->Hkv, N, cache->d);

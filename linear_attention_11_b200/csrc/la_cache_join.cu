@@ -22,11 +22,12 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttendParams p,
   const int4 tail = p.tails[blockIdx.x];
   if (tail.x == 0) return;
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
+#pragma unroll 1
+  for (int r = blockIdx.y * kWarps + (threadIdx.x >> 5); r < g.rows; r += gridDim.y * kWarps) {
   const int block = r / g.tile_rows, rr = r % g.tile_rows;
   const int64_t i = ((int64_t)tail.w * g.blocks + block) * g.tile_tokens + rr / p.G;
   const int64_t nq = p.q_len ? (int64_t)p.q_len[tail.y] : p.N;
-  if (rr >= g.tile_tokens * p.G || i >= nq) return;
+  if (rr >= g.tile_tokens * p.G || i >= nq) continue;
 
   const int n = tail.x + 1;
   const int64_t stride = (int64_t)g.rows * (D + kPartStats);  // floats of a part
@@ -81,6 +82,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const AttendParams p,
 #pragma unroll
   for (int j = 0; j < V; j += 2) dst[j / 2] = pack2<T>(o[j] * inv * v, o[j + 1] * inv * v);
   if (p.lse && lane == 0) p.lse[row] = (m - kAttendShift + log2f(l)) * kLn2;
+  }
 }
 
 template <typename T>
@@ -89,7 +91,7 @@ cudaError_t launch_typed(const AttendParams& p, const JoinGeometry& g, int d, in
   // a programmatic dependent of the attention kernel: its blocks are placed
   // while that one drains
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (g.rows + kWarps - 1) / kWarps);
+  cfg.gridDim = dim3(ctas, g.rows <= 32 ? g.rows / kWarps : g.rows / kWarps / 4);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

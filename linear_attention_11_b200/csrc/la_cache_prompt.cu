@@ -44,7 +44,7 @@ constexpr int kPlans = 4;               // units that the plan is ahead at most
 constexpr float kShift = kAttendShift;
 constexpr float kSlack = 8.f;  // growth of a row's maximum that is let pass
 // registers of a thread after the split; 640 x 96 at launch
-constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 56;
+constexpr int kRegsSoftmax = 128, kRegsConvert = 80, kRegsIssue = 56;
 static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= 640 * 96, "registers");
 
 // A block's part of a unit, as the planning warp writes it down.
@@ -83,7 +83,7 @@ struct Walk {
   int b, h, qt;
   int tile, tiles;
   int kv, nq, tpt;
-  bool ok;
+  bool ok, whole;  // whole: units are not cut, `pos` counts them, every gridDim.x-th
 
   __device__ void load(const AttendParams& p) {
     const int64_t len = p.kv_len[b], n = p.q_len ? (int64_t)p.q_len[b] : p.N;
@@ -102,10 +102,31 @@ struct Walk {
   __device__ int tiles_of(int q) const {
     return max(1, max(sees(q, 0), sees(q, 1)));
   }
-  __device__ int count() const { return (int)min((int64_t)(tiles - tile), end - pos); }
+  __device__ int count() const {
+    return whole ? tiles : (int)min((int64_t)(tiles - tile), end - pos);
+  }
   // the score tiles of row tile t in this share's n key tiles of the unit
   __device__ int count(int t, int n) const { return max(0, min(n, sees(qt, t) - tile)); }
+  // whole units: from unit `pos` on to the next of this block's that there is
+  __device__ void settle(const AttendParams& p) {
+    const int most = ((int)p.N + 2 * tpt - 1) / (2 * tpt);  // of a sequence and head
+    for (; pos < end; pos += gridDim.x) {
+      const int bh = (int)pos / most;
+      qt = (int)pos - bh * most;
+      b = bh / p.Hkv;
+      h = bh - b * p.Hkv;
+      load(p);
+      if (qt >= units()) continue;
+      tiles = tiles_of(qt);
+      return;
+    }
+  }
   __device__ void next(const AttendParams& p) {
+    if (whole) {
+      pos += gridDim.x;
+      settle(p);
+      return;
+    }
     pos += tiles - tile;
     tile = 0;
     if (++qt >= units()) {
@@ -152,7 +173,7 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 f) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams p, bool whole) {
   using L = PromptLayout<D>;
   constexpr uint32_t IDESC_QK = idesc_f16_f32(128, kKeys, 0);
   constexpr uint32_t IDESC_PV = idesc_f16_f32(128, D, 1);
@@ -178,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    p.tails[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!whole) p.tails[blockIdx.x] = make_int4(0, 0, 0, 0);
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(&kv_full[i], kConvert / 32);
       mbar_init(&kv_empty[i], 1);
@@ -208,9 +229,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   const int tpt = 128 / p.G;
   Walk w;
   w.tpt = tpt;
+  w.whole = whole;
   int64_t total;
-  Shares shares(0, 0, 1);
-  {
+  Shares shares(0, 0);
+  if (whole) {
+    w.tile = 0;
+    w.pos = blockIdx.x;
+    w.end = (int64_t)p.B * p.Hkv * ((p.N + 2 * tpt - 1) / (2 * tpt));
+    if (warp == kPlan) w.settle(p);
+  } else {
     int64_t* line = reinterpret_cast<int64_t*>(sm);  // [B] <= kAttendMaxBatch, before any tile
     for (w.b = warp; w.b < p.B; w.b += kThreads / 32) {
       w.load(p);
@@ -226,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += line[b];
     int64_t before = block_exclusive_sum<kThreads>(mine, misc, total);
-    shares = Shares(total, gridDim.x, 2);
+    shares = Shares(total, gridDim.x);
     w.pos = w.end = 0;
     if ((int)blockIdx.x < shares.n) {
       w.pos = shares.begin(blockIdx.x);
@@ -330,23 +357,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
             if ((rows >> r) & 1)
               x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at * D) + piece);
           }
+          // (the rows' maxima side by side: one after the other they took most of 6000
+          // cycles)
+          float top[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            top[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = unpack2<T>(u[k]);
+              top[i] = max3(top[i], fabsf(v.x), fabsf(v.y));
+            }
+          }
+#pragma unroll
+          for (int k = LPR / 2; k > 0; k >>= 1)
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+              top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], k));
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int ex = (int)(__float_as_uint(top[i]) >> 23) - 127;
+            top[i] = top[i] > 0.f && ex < 128 ? pow2i(max(min(14 - ex, 127), -126)) : 1.f;
+            const float mine1 = __shfl_sync(0xffffffffu, top[i], (lane % RPI) * LPR);
+            if (lane / RPI == i0 + i) up = mine1;
+          }
 #pragma unroll
           for (int i = 0; i < BATCH; ++i) {
             const int r = (warp & 3) * 32 + (i0 + i) * RPI + sub;
             const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 v = unpack2<T>(u[k]);
-              top = max3(top, fabsf(v.x), fabsf(v.y));
-            }
-#pragma unroll
-            for (int k = LPR / 2; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-            const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-            const float f1 = top > 0.f && ex < 128 ? pow2i(max(min(14 - ex, 127), -126)) : 1.f;
-            const float mine1 = __shfl_sync(0xffffffffu, f1, (lane % RPI) * LPR);
-            if (lane / RPI == i0 + i) up = mine1;
-            const float q1 = p.scale < 0.f ? -f1 : f1;
+            const float q1 = p.scale < 0.f ? -top[i] : top[i];
             uint32_t v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -492,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       }
       if (whole) {
         __syncwarp();
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < LPR; ++i) {
           const int r1 = i * RPI + sub, r = (warp & 3) * 32 + r1;
           const int64_t at = __shfl_sync(0xffffffffu, row, r1);
@@ -775,24 +815,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const AttendParams& p, int ctas, cudaStream_t stream) {
+cudaError_t launch_typed(const AttendParams& p, int ctas, bool whole, cudaStream_t stream) {
   constexpr int bytes = PromptLayout<D>::kBytes;
   static_assert(bytes <= 227 * 1024, "shared memory");
   const cudaError_t e = allow_shared<prompt_kernel<T, D>>(bytes);
   if (e != cudaSuccess) return e;
-  prompt_kernel<T, D><<<ctas, kThreads, bytes, stream>>>(p);
+  prompt_kernel<T, D><<<ctas, kThreads, bytes, stream>>>(p, whole);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache_prompt(const AttendParams& p, la_dtype dtype, int d, int ctas,
+cudaError_t launch_cache_prompt(const AttendParams& p, la_dtype dtype, int d, int ctas, bool whole,
                                 cudaStream_t stream) {
   if (d == 64)
-    return dtype == LA_BF16 ? launch_typed<__nv_bfloat16, 64>(p, ctas, stream)
-                            : launch_typed<__half, 64>(p, ctas, stream);
-  return dtype == LA_BF16 ? launch_typed<__nv_bfloat16, 128>(p, ctas, stream)
-                          : launch_typed<__half, 128>(p, ctas, stream);
+    return dtype == LA_BF16 ? launch_typed<__nv_bfloat16, 64>(p, ctas, whole, stream)
+                            : launch_typed<__half, 64>(p, ctas, whole, stream);
+  return dtype == LA_BF16 ? launch_typed<__nv_bfloat16, 128>(p, ctas, whole, stream)
+                          : launch_typed<__half, 128>(p, ctas, whole, stream);
 }
 
 }  // namespace la

@@ -102,7 +102,7 @@ struct Walk {
   int tile;          // its place in the unit
   int tiles;         // tiles of the unit (0: sequence without work)
   int kv, nq;        // its lengths
-  bool whole;        // units are not cut: each is one step of the line
+  bool whole;        // units are not cut: `pos` counts units, every gridDim.x-th
 
   __device__ void load(const AttendParams& p) {
     const int64_t len = p.kv_len[b], n = p.q_len ? (int64_t)p.q_len[b] : p.N;
@@ -111,15 +111,27 @@ struct Walk {
     nq = (int)n;
     tiles = ok && n > 0 ? max(1, (int)((len + kTile - 1) / kTile)) : 0;
   }
-  // the length of the line that a unit of this sequence takes
-  __device__ int length() const { return whole ? min(tiles, 1) : tiles; }
   // the unit's tiles in this share: from `tile`, as many as returned
   __device__ int count() const {
     return whole ? tiles : (int)min((int64_t)(tiles - tile), end - pos);
   }
+  // whole units: from unit `pos` on to the next of this block's that has work
+  __device__ void settle(const AttendParams& p) {
+    for (; pos < end; pos += gridDim.x) {
+      b = (int)pos / p.Hkv;
+      h = (int)pos - b * p.Hkv;
+      load(p);
+      if (tiles) return;
+    }
+  }
   // on to the next unit that has tiles (the share goes on)
   __device__ void next(const AttendParams& p) {
-    pos += length() - tile;
+    if (whole) {
+      pos += gridDim.x;
+      settle(p);
+      return;
+    }
+    pos += tiles - tile;
     tile = 0;
     if (++h < p.Hkv) return;
     h = 0;
@@ -171,21 +183,29 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     fence_barrier_init();
   }
 
-  // The line's length, this block's share of it, and the unit where that begins.
+  // The line's length, this block's share of it, and the unit where that begins; whole
+  // units are counted out.
   Walk w;
   int64_t total;
-  Shares shares(0, 0, 1);
+  Shares shares(0, 0);
   w.whole = whole;
-  {
+  if (whole) {
+    w.tile = 0;
+    w.pos = blockIdx.x;
+    w.end = (int64_t)p.B * p.Hkv;
+    w.settle(p);
+    __syncthreads();  // barriers are set up
+    if (w.pos >= w.end) return;
+  } else {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
     int64_t mine = 0;
     for (w.b = b0; w.b < b1; ++w.b) {
       w.load(p);
-      mine += (int64_t)w.length() * p.Hkv;
+      mine += (int64_t)w.tiles * p.Hkv;
     }
     int64_t before = block_exclusive_sum<kThreads>(mine, misc, total);
-    shares = Shares(total, gridDim.x, whole ? 1 : 2);
+    shares = Shares(total, gridDim.x);
     w.pos = w.end = 0;
     if ((int)blockIdx.x < shares.n) {
       w.pos = shares.begin(blockIdx.x);
@@ -194,16 +214,16 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
       for (w.b = b0;; ++w.b) {
         w.load(p);
-        if (w.pos < before + (int64_t)w.length() * p.Hkv) break;
-        before += (int64_t)w.length() * p.Hkv;
+        if (w.pos < before + (int64_t)w.tiles * p.Hkv) break;
+        before += (int64_t)w.tiles * p.Hkv;
       }
       misc[6] = w.b;
-      misc[7] = div_short(w.pos - before, w.length());
-      misc[8] = w.pos - before - misc[7] * w.length();
+      misc[7] = div_short(w.pos - before, w.tiles);
+      misc[8] = w.pos - before - misc[7] * w.tiles;
     }
     __syncthreads();
     if (w.pos >= w.end) {
-      if (threadIdx.x == 0 && !whole) p.tails[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (threadIdx.x == 0) p.tails[blockIdx.x] = make_int4(0, 0, 0, 0);
       griddep_launch_dependents();
       return;
     }

@@ -148,7 +148,7 @@ cudaError_t launch_cache_read(const la_cache& c, const int32_t* table, const int
                               cudaStream_t stream);
 // Whether an attention call over page tables of `tokens` tokens a sequence uses its
 // workspace.
-bool attend_uses_workspace(int G, int64_t N, int64_t tokens);
+bool attend_uses_workspace(int B, int Hkv, int G, int64_t N, int d, int64_t tokens, int sms);
 size_t attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d, int sms);
 cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype,
                                 const int32_t* table, const int32_t* kv_len, const int32_t* q_len,
