@@ -321,7 +321,7 @@ la_status la_decode_steps(float *S, const la_bf16 *q, const la_bf16 *k, const la
  * Sequence b's token t is row t % page of page table[b][t / page]; table is
  * [B, max_pages] int32.  Only the entries that a call's tokens need are read, so
  * the rest may hold anything.  Pages may be shared by sequences that only read
- * them (a common prompt); a page that a call writes must belong to one sequence.
+ * them (a common prompt); a page that a call writes must belong to one sequence, once.
  *
  * Lengths (start, count, kv_len, q_len) are int32 [B] device arrays, so a
  * captured graph follows them as they change; a null count or q_len stands for N
@@ -330,7 +330,8 @@ la_status la_decode_steps(float *S, const la_bf16 *q, const la_bf16 *k, const la
  * it is written), a page number out of range is not followed (its tokens are
  * not written, or taken as zeros), and LA_DEV_BAD_INDEX is set.
  *
- * page in {16, 32, 64, 128}, d in {64, 128}; num_pages * Hkv * page < 2^31.
+ * page in {16, 32, 64, 128}, d in {64, 128}; num_pages * Hkv * page < 2^31; a
+ * sequence has at most 2^31 - 2^16 tokens.
  * ---------------------------------------------------------------------- */
 typedef enum { LA_BF16 = 0, LA_FP16 = 1, LA_F32 = 2 } la_dtype;
 

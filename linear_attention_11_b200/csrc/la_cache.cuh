@@ -131,6 +131,12 @@ __device__ __forceinline__ float pow2i(int e) {  // 2^e, -126 <= e <= 127
 }
 
 // ---------------------------------------------------------------- lengths
+// Tokens that a sequence can have: its pages', and no more than leave the sums of a
+// token and a tile in 32 bits.
+__device__ __forceinline__ int64_t token_limit(int max_pages, int page_log2) {
+  return min((int64_t)max_pages << page_log2, (int64_t)0x7fff0000);
+}
+
 // Tokens [first, first + n) of a sequence: false (and the status bit) when they
 // do not lie in [0, limit); n = 0 is always well.
 __device__ __forceinline__ bool token_range_ok(int64_t first, int64_t n, int64_t nmax,
@@ -161,7 +167,7 @@ struct AttendParams {
 
 // Whether a sequence's lengths lie in range; if not the sequence is left out.
 __device__ __forceinline__ bool attend_lengths_ok(int64_t kv, int64_t nq, const AttendParams& p) {
-  const bool ok = kv >= 0 && kv <= ((int64_t)p.max_pages << p.page_log2) && nq >= 0 && nq <= p.N;
+  const bool ok = kv >= 0 && kv <= token_limit(p.max_pages, p.page_log2) && nq >= 0 && nq <= p.N;
   if (!ok) atomicOr(p.status, kDevBadIndex);
   return ok;
 }

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512)
   const int b = (int)(bh / (uint32_t)p.Hkv), h = (int)(bh - (uint32_t)b * p.Hkv);
 
   const int64_t start = p.start[b], count = p.count ? (int64_t)p.count[b] : p.N;
-  if (!token_range_ok(start, count, p.N, (int64_t)p.max_pages << p.page_log2, p.status)) return;
+  if (!token_range_ok(start, count, p.N, token_limit(p.max_pages, p.page_log2), p.status)) return;
   const int64_t block = (start >> p.page_log2) + s;  // page of the sequence
   const int64_t first = block << p.page_log2;        // its first token
   const int64_t lo = max(start, first), hi = min(start + count, first + p.page);
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p
   const int64_t row0 = (int64_t)(unit - bh * p.blocks) * ROWS;
   const int b = (int)(bh / (uint32_t)p.Hkv), h = (int)(bh - (uint32_t)b * p.Hkv);
   const int64_t start = p.start[b], count = p.count ? (int64_t)p.count[b] : p.N;
-  if (!token_range_ok(start, count, p.N, (int64_t)p.max_pages << p.page_log2, p.status)) return;
+  if (!token_range_ok(start, count, p.N, token_limit(p.max_pages, p.page_log2), p.status)) return;
   if (row0 >= count) return;
   const int rows = (int)min((int64_t)ROWS, count - row0);
   const int tok0 = (int)(start + row0), page0 = tok0 >> p.page_log2;

@@ -285,6 +285,53 @@ def test_attend_leaves_bad_lengths_out_and_follows_no_bad_page(la, N):
     assert la.la_device_status() == (0, 2)
 
 
+def test_lengths_at_the_end_of_32_bits_are_left_out(la):
+    """A table of 2^31 tokens: lengths whose sums would pass 32 bits are refused, not followed."""
+    page, big = 128, 2 ** 31 - 1
+    cache, _ = filled_cache([page], 1, page, 64, 21)
+    dev = to_device(la, cache, DEV)
+    t = torch.zeros(1, 2 ** 31 // page, dtype=torch.int32, device=DEV)
+    for N in (1, 40):
+        q = normal(1, 1, 1, N, 64).half().to(DEV)
+        o = torch.full_like(q, 5.0)
+        la.la_cache_attend(q, dev, t, ints([big], DEV), o=o)
+        assert (o == 5).all() and la.la_device_status() == (0, 2)
+        k = [torch.full_like(q, 5.0) for _ in "kv"]
+        la.la_cache_read(dev, t, ints([big - 1], DEV), *k)
+        assert (k[0] == 5).all() and la.la_device_status() == (0, 2)
+        la.la_cache_write(*k, dev, t, ints([big - 1], DEV))
+        assert la.la_device_status() == (0, 2)
+    same_cache(from_device(dev), cache)
+
+
+def test_two_captured_graphs_with_a_workspace_each(la):
+    """Graphs captured from one call each, replayed in turn and together on two streams."""
+    cache, table = filled_cache([3000, 2000], 1, 16, 64, 22)
+    dev, t, lens = to_device(la, cache, DEV), torch.from_numpy(table).to(DEV), ints([3000, 2000], DEV)
+    qs = [normal(i, 2, 4, N, 64).half().to(DEV) for i, N in enumerate((2, 60))]
+    refs = [la.la_cache_attend(q, dev, t, lens) for q in qs]
+    need = [la.la_cache_attend_workspace_bytes(2, 4, 1, q.shape[2], 64) for q in qs]
+    work = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in need]
+    outs, graphs, streams = [torch.zeros_like(q) for q in qs], [], [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for q, o, ws, s in zip(qs, outs, work, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            la.la_cache_attend(q, dev, t, lens, o=o, workspace=ws, stream=s)
+        graphs.append(g)
+    for rounds in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, ref in zip(outs, refs):
+            assert torch.equal(o, ref)
+    clean(la)
+
+
 @pytest.mark.parametrize("N", [1, 64])
 def test_shared_pages_and_the_same_bits(la, N):
     """Two sequences on the pages of one prompt; repeated calls give the same bits."""
@@ -439,6 +486,20 @@ def test_two_streams_at_once(la):
     for ref, o in zip(refs, outs):
         assert all(torch.equal(x, ref) for x in o)
     clean(la)
+
+
+@pytest.mark.parametrize("G,Hkv,N", [(4, 2, 1), (5, 3, 4), (32, 1, 1), (7, 2, 9), (24, 1, 40), (1, 3, 200)])
+def test_cut_units_are_whole_ones(la, G, Hkv, N):
+    """The same call over a table of the sequences' own length (units whole, where short) and over
+    one with room for far more (the general way)."""
+    kv = [N + 100, N, N + 211, 1, 260]
+    nq = [N, N, max(1, N - 1), 1, 1]
+    cache, table = filled_cache(kv, Hkv, 16, 64, G)
+    q = normal(N, 5, Hkv * G, N, 64).half()
+    wide = np.full((5, 4096), -1, dtype=np.int32)
+    wide[:, :table.shape[1]] = table
+    attend_both(la, cache, table, q, kv, nq, what="short table")
+    attend_both(la, cache, wide, q, kv, nq, what="wide table")
 
 
 @pytest.mark.parametrize("d,G", [(64, 3), (128, 4)])
