@@ -81,7 +81,8 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
 struct Walk {
   int64_t pos, end;
   int b, h, qt;
-  int tile, tiles;
+  Place at;
+  int tiles;
   int kv, nq, tpt;
   bool ok, whole;  // whole: units are not cut, `pos` counts them, every gridDim.x-th
 
@@ -102,11 +103,11 @@ struct Walk {
   __device__ int tiles_of(int q) const {
     return max(1, max(sees(q, 0), sees(q, 1)));
   }
-  __device__ int count() const {
-    return whole ? tiles : (int)min((int64_t)(tiles - tile), end - pos);
-  }
+  __device__ int places(int q) const { return tiles_of(q) + kUnitCost; }
+  __device__ int tile() const { return whole ? 0 : at.tile(); }
+  __device__ int count() const { return whole ? tiles : at.count(tiles, end - pos); }
   // the score tiles of row tile t in this share's n key tiles of the unit
-  __device__ int count(int t, int n) const { return max(0, min(n, sees(qt, t) - tile)); }
+  __device__ int count(int t, int n) const { return max(0, min(n, sees(qt, t) - tile())); }
   // whole units: from unit `pos` on to the next of this block's that there is
   __device__ void settle(const AttendParams& p) {
     const int most = ((int)p.N + 2 * tpt - 1) / (2 * tpt);  // of a sequence and head
@@ -127,8 +128,10 @@ struct Walk {
       settle(p);
       return;
     }
-    pos += tiles - tile;
-    tile = 0;
+    pos += tiles + kUnitCost - at.x;
+    at.x = 0;
+    if (pos + kUnitCost >= end) pos = end;  // the share ends before the next one's first tile
+    if (pos >= end) return;
     if (++qt >= units()) {
       qt = 0;
       if (++h >= p.Hkv) {
@@ -233,7 +236,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   int64_t total;
   Shares shares(0, 0);
   if (whole) {
-    w.tile = 0;
     w.pos = blockIdx.x;
     w.end = (int64_t)p.B * p.Hkv * ((p.N + 2 * tpt - 1) / (2 * tpt));
     if (warp == kPlan) w.settle(p);
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     for (w.b = warp; w.b < p.B; w.b += kThreads / 32) {
       w.load(p);
       int64_t sum = 0;
-      for (int q = lane; q < w.units(); q += 32) sum += w.tiles_of(q);
+      for (int q = lane; q < w.units(); q += 32) sum += w.places(q);
 #pragma unroll
       for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
       if (lane == 0) line[w.b] = sum * p.Hkv;
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       int64_t rest = misc[22];
       int found = -1;
       for (int q0 = 0; found < 0; q0 += 32) {
-        const int n = q0 + lane < w.units() ? w.tiles_of(q0 + lane) : 0;
+        const int n = q0 + lane < w.units() ? w.places(q0 + lane) : 0;
         int in = n;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -292,8 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         }
       }
       w.qt = found;
-      w.tile = (int)rest;
+      w.at.x = (int)rest;
       w.tiles = w.tiles_of(found);
+      if (w.count() == 0) w.next(p);  // a share that ends, or goes on, behind this unit's cost
     }
   }
   tc_fence_before();
@@ -344,9 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         // scale goes here too, so that the scores' factor is not negative.  The warp
         // reads its 32 rows together, RPI at a time, and hands each row's factor to
         // the lane that owns it.
-        constexpr int BATCH = 8;
+        constexpr int BATCH = 4;
         float up = 1.f;
-#pragma unroll
+#pragma unroll 1
         for (int i0 = 0; i0 < LPR; i0 += BATCH) {
           uint4 x[BATCH];
 #pragma unroll
@@ -756,11 +759,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         if (more) {
           // the largest scales among the pages of these tiles
           const int n = w.count(), c = max(w.count(0, n), w.count(1, n));
-          const int stop = min(w.kv, (w.tile + c) * kKeys);
-          const int g1 = stop > w.tile * kKeys ? ((stop - 1) >> p.page_log2) + 1 : 0;
+          const int t0 = w.tile(), stop = min(w.kv, (t0 + c) * kKeys);
+          const int g1 = stop > t0 * kKeys ? ((stop - 1) >> p.page_log2) + 1 : 0;
           const int* ids = p.table + (int64_t)w.b * p.max_pages;
 #pragma unroll 4
-          for (int g = ((w.tile * kKeys) >> p.page_log2) + lane; g < g1; g += 32) {
+          for (int g = ((t0 * kKeys) >> p.page_log2) + lane; g < g1; g += 32) {
             const int id = __ldg(ids + g);
             if (id >= 0 && id < p.num_pages) {
               ek = fmaxf(ek, __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + w.h));
@@ -782,16 +785,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
             unit.b = w.b;
             unit.h = w.h;
             unit.qt = w.qt;
-            unit.tile = w.tile;
+            unit.tile = w.tile();
             unit.n = n;
             unit.c[0] = w.count(0, n);
             unit.c[1] = w.count(1, n);
             unit.kv = w.kv;
             unit.nq = w.nq;
-            unit.begins = w.tile == 0;
-            unit.ends = w.tile + n == w.tiles;
+            unit.begins = w.tile() == 0;
+            unit.ends = w.tile() + n == w.tiles;
             unit.follow =
-                unit.begins && !unit.ends ? shares.behind(blockIdx.x, w.pos + w.tiles) : 0;
+                unit.begins && !unit.ends ? shares.behind(blockIdx.x, w.pos + w.tiles + kUnitCost - w.at.x)
+                                           : 0;
             unit.ek = ek;
             unit.ev = ev;
           }

@@ -95,11 +95,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// A block's walk along its share [pos, end) of the line of tiles.
+// A block's walk along its share [pos, end) of the line.
 struct Walk {
-  int64_t pos, end;  // the share's next tile and its end
-  int b, h;          // unit of the next tile
-  int tile;          // its place in the unit
+  int64_t pos, end;  // the next place and the share's end
+  int b, h;          // unit of that place
+  Place at;          // where in the unit
   int tiles;         // tiles of the unit (0: sequence without work)
   int kv, nq;        // its lengths
   bool whole;        // units are not cut: `pos` counts units, every gridDim.x-th
@@ -111,10 +111,11 @@ struct Walk {
     nq = (int)n;
     tiles = ok && n > 0 ? max(1, (int)((len + kTile - 1) / kTile)) : 0;
   }
-  // the unit's tiles in this share: from `tile`, as many as returned
-  __device__ int count() const {
-    return whole ? tiles : (int)min((int64_t)(tiles - tile), end - pos);
-  }
+  // places that a unit of this sequence takes
+  __device__ int places() const { return tiles ? tiles + kUnitCost : 0; }
+  __device__ int tile() const { return whole ? 0 : at.tile(); }
+  // the unit's tiles in this share: from tile(), as many as returned
+  __device__ int count() const { return whole ? tiles : at.count(tiles, end - pos); }
   // whole units: from unit `pos` on to the next of this block's that has work
   __device__ void settle(const AttendParams& p) {
     for (; pos < end; pos += gridDim.x) {
@@ -124,15 +125,17 @@ struct Walk {
       if (tiles) return;
     }
   }
-  // on to the next unit that has tiles (the share goes on)
+  // on to the next unit that has tiles (the share goes on, or ends before its first)
   __device__ void next(const AttendParams& p) {
     if (whole) {
       pos += gridDim.x;
       settle(p);
       return;
     }
-    pos += tiles - tile;
-    tile = 0;
+    pos += places() - at.x;
+    at.x = 0;
+    if (pos + kUnitCost >= end) pos = end;
+    if (pos >= end) return;
     if (++h < p.Hkv) return;
     h = 0;
     do {
@@ -190,7 +193,6 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
   Shares shares(0, 0);
   w.whole = whole;
   if (whole) {
-    w.tile = 0;
     w.pos = blockIdx.x;
     w.end = (int64_t)p.B * p.Hkv;
     w.settle(p);
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     int64_t mine = 0;
     for (w.b = b0; w.b < b1; ++w.b) {
       w.load(p);
-      mine += (int64_t)w.tiles * p.Hkv;
+      mine += (int64_t)w.places() * p.Hkv;
     }
     int64_t before = block_exclusive_sum<kThreads>(mine, misc, total);
     shares = Shares(total, gridDim.x);
@@ -214,12 +216,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     if (w.pos < w.end && before <= w.pos && w.pos < before + mine) {
       for (w.b = b0;; ++w.b) {
         w.load(p);
-        if (w.pos < before + (int64_t)w.tiles * p.Hkv) break;
-        before += (int64_t)w.tiles * p.Hkv;
+        if (w.pos < before + (int64_t)w.places() * p.Hkv) break;
+        before += (int64_t)w.places() * p.Hkv;
       }
       misc[6] = w.b;
-      misc[7] = div_short(w.pos - before, w.tiles);
-      misc[8] = w.pos - before - misc[7] * w.tiles;
+      misc[7] = div_short(w.pos - before, w.places());
+      misc[8] = w.pos - before - misc[7] * w.places();
     }
     __syncthreads();
     if (w.pos >= w.end) {
@@ -229,8 +231,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     }
     w.b = (int)misc[6];
     w.h = (int)misc[7];
-    w.tile = (int)misc[8];
+    w.at.x = (int)misc[8];
     w.load(p);
+    if (w.count() == 0) w.next(p);  // a share that ends, or goes on, behind this unit's cost
   }
 
   if (warp == 4) {
@@ -264,11 +267,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       auto page_at = [&](int group) {  // page of 16-token group `group` of the unit (-2: none)
         return (int64_t)group * 16 < w.kv ? row[group >> (p.page_log2 - 4)] : -2;
       };
-      int ahead = page_at(w.tile * 4 + lane);
+      int ahead = page_at(w.tile() * 4 + lane);
       int id = -2;
       float ks = 0.f, vs = 0.f;
       for (int i = 0; i < n && go; ++i, ++it) {
-        const int t = w.tile + i;
+        const int t = w.tile() + i;
         if ((i & 7) == 0) {
           id = ahead;
           if (i + 8 < n) ahead = page_at((t + 8) * 4 + lane);
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
   int unit = 0;
   for (; w.pos < w.end && ok; ++unit) {
     const int n = w.count();
-    const int R = w.nq * p.G;
+    const int R = w.nq * p.G, first_tile = w.tile();
     ok = warp_wait(&q_full[unit & 1], (unit >> 1) & 1, p.status, abort_flag);
     if (!ok) break;
     // q: rows as f16 operand pieces in shared memory, with each row's factor.  Eight
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       ok = warp_wait(&full[s], (it / L::kStages) & 1, p.status, abort_flag);
       if (!ok) break;
       const int g0 = (warp & 1) * SUB;          // first of this warp's groups
-      const int t0 = (w.tile + i) * kTile + g0 * 16;      // and its first token
+      const int t0 = (first_tile + i) * kTile + g0 * 16;      // and its first token
       if (t0 >= w.kv) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
 
     // the four warps' parts of the unit into one: each writes its own, and all
     // threads add them up
-    const bool begins = w.tile == 0, ends = w.tile + n == w.tiles;
+    const bool begins = first_tile == 0, ends = first_tile + n == w.tiles;
     float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * L::kRows * (D + kPartStats);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -632,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       }
     }
     if (begins && !ends) {
-      tail = make_int4(shares.behind(blockIdx.x, w.pos + w.tiles), w.b, w.h, 0);
+      tail = make_int4(shares.behind(blockIdx.x, w.pos + w.places() - w.at.x), w.b, w.h, 0);
     }
     w.next(p);  // (what this unit left in shared memory is written again after the next sync)
   }
