@@ -185,7 +185,8 @@ __device__ __forceinline__ bool attend_lengths_ok(int64_t kv, int64_t nq, const 
 //   scale v of the values), then for each row {m, l, v, 0}, m in log2 units
 constexpr int kPartStats = 4;
 // In tiles: about 5000 cycles against 1200 (tokens), 18000 against 4300 (prompts).
-// Without it blocks whose share is many short units ended last (XX).
+// Without it blocks whose share is many short units ended last (3 prompts of 2510
+// tokens, 32 heads in groups of eight: 368 us instead of 231).
 constexpr int kUnitCost = 4;
 
 // A block's place on the line: place `x` of a unit of `tiles` tiles, `left` places from
