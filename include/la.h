@@ -382,7 +382,12 @@ la_status la_cache_read(const la_cache *cache, const int32_t *table, const int32
  *   q, o      bf16 or fp16 [B,Hq,N,d], o not overlapping q or the cache
  *   lse       fp32 [B,Hq,N], or null
  *   scale     finite; usually 1/sqrt(d)
- * Scores, the softmax's sums and the products are held in fp32.
+ * Scores, the softmax's sums and the products' sums are held in fp32; weights, and
+ * codes times scales, enter the products as fp16, relative to the largest weight of
+ * the row and the largest scale among the sequence's pages of the head.  A page whose
+ * scale is 2^-15 of that or more counts exactly, a smaller one to 2^-25 of it (a row
+ * that sees only such pages keeps no more of them), a weight to 2^-32 of the row's
+ * largest.
  * Splits long sequences over the SMs and joins the parts; the parts' workspace
  * comes from the stream-ordered pool (la_cache_attend) or from the caller
  * (la_cache_attend_ws: 256-byte aligned, at least
