@@ -479,7 +479,8 @@ def la_cache_attend(q, cache: la_cache, table, kv_len, q_len=None, o=None, lse=N
                     scale: float | None = None, workspace=None, stream=None):
     """Causal softmax attention of the last q_len[b] (or N) of kv_len[b] cached tokens:
     q [B,Hq,N,d] bf16 or fp16 -> o; lse [B,Hq,N] fp32, if given, is written; scale
-    defaults to 1/sqrt(d).  With a workspace (CUDA, contiguous) the call is
+    defaults to 1/sqrt(d).  Rows behind q_len[b] are left as they were: what they hold in
+    a new o is undefined.  With a workspace (CUDA, contiguous) the call is
     la_cache_attend_ws."""
     fn = "la_cache_attend" if workspace is None else "la_cache_attend_ws"
     c = _cache(fn, cache, table, {"kv_len": kv_len, "q_len": q_len},

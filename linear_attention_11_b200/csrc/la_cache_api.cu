@@ -12,6 +12,8 @@
 namespace la {
 namespace {
 
+constexpr int64_t kMaxCallTokens = 0x7fffffff - 256;  // tokens of a call, in 32 bits
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 struct Range {
@@ -38,8 +40,8 @@ la_status check_cache(const la_cache* c, const int32_t* table, int B, int64_t N,
   if ((c->d != 64 && c->d != 128) ||
       (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128))
     return LA_ERR_UNSUPPORTED;
-  // rows of codes, and tokens of one call, take 32 bits
-  if (c->num_pages > 0x7fffffff / c->Hkv / c->page || N > 0x7fffffff - 256 ||
+  // rows of codes take 32 bits
+  if (c->num_pages > 0x7fffffff / c->Hkv / c->page || N > kMaxCallTokens ||
       (int64_t)B * c->Hkv > 0x7fffffff)
     return LA_ERR_INVALID_ARG;
   return LA_OK;
@@ -152,6 +154,9 @@ LA_EXPORT la_status la_cache_read(const la_cache* cache, const int32_t* table,
 
 LA_EXPORT size_t la_cache_attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || N <= 0 || (d != 64 && d != 128)) return 0;
+  if (Hq / Hkv > kAttendMaxGroup || B > kAttendMaxBatch || N > kMaxCallTokens ||
+      (int64_t)B * Hkv > 0x7fffffff)
+    return 0;
   const int sms = device_sms();
   return sms > 0 ? attend_workspace_bytes(B, Hq, Hkv, N, d, sms) : 0;
 }

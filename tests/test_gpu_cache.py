@@ -368,6 +368,13 @@ def test_workspace_of_the_caller(la):
     assert e.value.code == 5
 
 
+def test_workspace_sizes_of_calls_that_are_refused(la):
+    for bad in ((1, 66, 2, 8, 64), (1, 256, 1, 1, 128), (4097, 4, 4, 8, 64), (1, 4, 2, 2 ** 31 - 1, 64),
+                (4096, 1 << 20, 1 << 20, 1, 64)):
+        assert la.la_cache_attend_workspace_bytes(*bad) == 0, bad
+    assert la.la_cache_attend_workspace_bytes(4096, 64, 2, 2 ** 31 - 257, 64) > 0
+
+
 def test_offsets_beyond_32_bits(la):
     """A pool of more than 2^32 codes: the pages used lie at its end."""
     page, Hkv, d, n = 128, 4, 128, 300
