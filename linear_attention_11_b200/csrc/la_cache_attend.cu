@@ -26,7 +26,7 @@ Shape shape_of(int B, int Hkv, int G, int64_t N, int d, int64_t tokens, int sms)
   s.token = N * G <= kTokenRows;
   if (s.token) {
     s.whole = tokens <= kWholeTokens && (int64_t)B * Hkv <= 0x7fffffff - 65536;
-    s.rows = N * G <= 16 ? 16 : 32;
+    s.rows = N * G <= 8 ? 8 : N * G <= 16 ? 16 : 32;
     s.ctas = (d == 128 ? 2 : 3) * sms;
   } else {
     const int tpu = 2 * (128 / G);  // tokens of a unit
@@ -57,7 +57,7 @@ cudaError_t launch_cache_attend(const la_cache& c, const void* q, la_dtype dtype
   if (workspace)
     p.tails = reinterpret_cast<int4*>(static_cast<char*>(workspace) + part_bytes(s, c.d));
   const cudaError_t e = s.token
-                            ? launch_cache_token(p, c, dtype, (int)N * p.G, s.ctas, s.whole, stream)
+                            ? launch_cache_token(p, c, dtype, s.rows, s.ctas, s.whole, stream)
                             : launch_cache_prompt(p, dtype, c.d, s.ctas, s.whole, stream);
   if (e != cudaSuccess || s.whole) return e;
   const JoinGeometry g = s.token ? JoinGeometry{s.rows, 1, s.rows, (int)N}

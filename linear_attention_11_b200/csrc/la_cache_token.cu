@@ -21,6 +21,11 @@
 // - The products are mma.sync m16n8k16 (f16 in, fp32 sums): 16 rows at 2 R
 //   flops a byte are far from the tensor limits, and tcgen05 would need the
 //   converted tile in shared memory.
+// - Up to eight rows (FEW) are the 8-wide side of the products, S^T = K Q^T and
+//   O^T = V^T P^T: half the products, exponentials and sums of the other way round
+//   (more rows are its 16-wide side).  Weights come out of the first as tokens x rows
+//   and are turned by movmatrix.  256 sequences, groups of four: 231 us the other
+//   way, 206 this; a million tokens, 8 heads, one row each: 334 and 320.
 // - q is scaled by a power of two for each row so that its largest entry lies in
 //   [2^14, 2^15) before it is rounded to f16: exact down to 2^-28 of the largest.
 // - Weights go to f16 as 2^7 p b_j / v, v the largest value scale so far (a power
@@ -49,19 +54,22 @@ constexpr float kSlack = 8.f;   // growth of a row's maximum that is let pass
 // and the other two the next stage's; with two, all four take every stage, two for each
 // row group (a warp that held both groups' outputs would not fit its registers: rows
 // 32, 32 x 8 heads, up to 8192 tokens: 158 us against 113).
-template <int D, int RG>
+template <int D, int ROWS>
 struct TokenLayout {
-  static constexpr int kRows = 16 * RG;
+  static constexpr int RG = ROWS == 32 ? 2 : 1;
+  static constexpr int kRows = ROWS;
   static constexpr int kSub = 2;           // groups of 16 tokens that a warp takes at a time
   static constexpr int kSharers = 2 * RG;  // warps that read a stage
   static constexpr int kStages = D == 128 ? 5 - RG : 7 - RG;
+  // (of one unit a stage is always the same two warps', so they wait for each filling)
+  static_assert(RG == 2 || kStages % 2 == 0, "stages of two pairs of warps in turn");
   static constexpr int kHalf = kTile * D;             // bytes of a K or V tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kQOff = kStages * kStage;       // Q fragments
-  static constexpr int kRawOff = kQOff + RG * (D / 16) * 512;  // two units' q as they come
+  static constexpr int kRawOff = kQOff + ROWS * D * 2;  // two units' q as they come
   static constexpr int kRaw = kRows * D * 2;
   static constexpr int kBufOff = kRawOff + 2 * kRaw;
-  static constexpr int kBuf = 16 * (D + 4) * 4;         // a warp's fp32 output, rows padded
+  static constexpr int kBuf = ROWS / RG * (D + 4) * 4;  // a warp's fp32 output, rows padded
   static constexpr int kStatOff = kBufOff + 4 * kBuf;    // wm[4][16], wl[4][16], wv[4], rs[rows]
   static constexpr int kScaleOff = kStatOff + (8 * 16 + 4 + kRows) * 4;  // float2 [stages][4]
   static constexpr int kBarOff = (kScaleOff + kStages * 4 * 8 + 7) / 8 * 8;
@@ -75,6 +83,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// Of an 8 x 8 matrix of 16-bit numbers (lane 4 r + c: columns 2c, 2c + 1 of row r) the
+// transpose, likewise.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint64_t* bar, int c0,
@@ -146,11 +162,13 @@ struct Walk {
   }
 };
 
-template <typename T, int D, int RG>
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     token_kernel(const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const AttendParams p, int box, bool whole) {
-  using L = TokenLayout<D, RG>;
+  using L = TokenLayout<D, ROWS>;
+  constexpr int RG = L::RG;
+  constexpr bool FEW = ROWS == 8;
   constexpr int KS = D / 16;  // 16-wide steps of q . k
   constexpr int NB = D / 8;   // 8-wide blocks of the output
   constexpr int SUB = L::kSub;
@@ -238,13 +256,48 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
 
   if (warp == 4) {
     // ------------------------------------------------------------ copies
-    // A lane knows the page and scales of 16 tokens: 32 lanes, eight tiles ahead.
+    // A lane knows the page and scales of 16 tokens: 32 lanes, eight tiles.  They are
+    // asked for ahead, on across units: scales while the eight tiles before go by,
+    // page numbers another eight before that (32 x 8 heads, 32 rows: 125 us without,
+    // 122 with).
     if (lane == 0) {
       prefetch_tmap(&map_k);
       prefetch_tmap(&map_v);
     }
     const int per_box = box / 16;        // 16-token groups of a copy
     const uint32_t bytes = (uint32_t)box * D;
+    Walk ahead = w;   // the eight tiles whose page numbers are asked for next: of this
+    int ahead_at = 0;  // unit, from this of its tiles in the share on
+    auto ask_pages = [&](int& h) {  // page of the lane's tokens (-2: none), the unit's head
+      int id = -2;
+      h = ahead.h;
+      if (ahead.pos < ahead.end) {
+        const int64_t group = (int64_t)(ahead.tile() + ahead_at) * 4 + lane;
+        if (group * 16 < ahead.kv)
+          id = p.table[(int64_t)ahead.b * p.max_pages + (group >> (p.page_log2 - 4))];
+        ahead_at += 8;
+        if (ahead_at >= ahead.count()) {
+          ahead.next(p);
+          ahead_at = 0;
+        }
+      }
+      return id;
+    };
+    auto ask_scales = [&](int& id, int h, float& ks, float& vs) {
+      const bool known = id >= 0 && id < p.num_pages;
+      ks = -1.f;  // not a scale: the group's codes count as zero
+      vs = 0.f;
+      if (known) {
+        ks = __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + h);
+        vs = __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + h);
+      } else {
+        if (id != -2) atomicOr(p.status, kDevBadIndex);
+        id = -1;
+      }
+    };
+    int h1, h2, id1 = ask_pages(h1), id2 = ask_pages(h2);
+    float ks1, vs1;
+    ask_scales(id1, h1, ks1, vs1);
     int it = 0;
     bool go = true;
     int unit = 0, asked = 0;  // units; units whose q has been asked for
@@ -263,28 +316,17 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
                     static_cast<const T*>(p.q) + row * D, D * 2, &q_full[qs]);
         }
       }
-      const int* row = p.table + (int64_t)w.b * p.max_pages;
-      auto page_at = [&](int group) {  // page of 16-token group `group` of the unit (-2: none)
-        return (int64_t)group * 16 < w.kv ? row[group >> (p.page_log2 - 4)] : -2;
-      };
-      int ahead = page_at(w.tile() * 4 + lane);
-      int id = -2;
+      int id = -1;
       float ks = 0.f, vs = 0.f;
       for (int i = 0; i < n && go; ++i, ++it) {
         const int t = w.tile() + i;
         if ((i & 7) == 0) {
-          id = ahead;
-          if (i + 8 < n) ahead = page_at((t + 8) * 4 + lane);
-          const bool known = id >= 0 && id < p.num_pages;
-          ks = -1.f;  // not a scale: the group's codes count as zero
-          vs = 0.f;
-          if (known) {
-            ks = __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + w.h);
-            vs = __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + w.h);
-          } else {
-            if (id != -2) atomicOr(p.status, kDevBadIndex);
-            id = -1;
-          }
+          id = id1;
+          ks = ks1;
+          vs = vs1;
+          id1 = id2;
+          ask_scales(id1, h2, ks1, vs1);
+          id2 = ask_pages(h2);
         }
         const int s = it % L::kStages;
         if (it >= L::kStages)
@@ -337,40 +379,41 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     const int R = w.nq * p.G, first_tile = w.tile();
     ok = warp_wait(&q_full[unit & 1], (unit >> 1) & 1, p.status, abort_flag);
     if (!ok) break;
-    // q: rows as f16 operand pieces in shared memory, with each row's factor.  Eight
-    // threads a row, D / 8 values each.  The sign of the scale goes into q, so that
-    // the factor is not negative.
+    // q: rows as f16 operand pieces in shared memory, with each row's factor.  TPR
+    // threads a row.  The sign of the scale goes into q, so that the factor is not
+    // negative.
+    constexpr int TPR = kConsumers / (ROWS / RG), V = D / TPR;  // threads and a thread's values
 #pragma unroll
     for (int mt = 0; mt < RG; ++mt) {
-      const int r = mt * 16 + (threadIdx.x >> 3), e = threadIdx.x & 7;
-      float x[D / 8];
+      const int r = mt * 16 + threadIdx.x / TPR, e = threadIdx.x % TPR;
+      const uint32_t from = base + L::kRawOff + (unit & 1) * L::kRaw + r * D * 2 + e * V * 2;
+      float x[V];
       float top = 0.f;
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        uint4 q4 = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R) q4 = lds128(base + L::kRawOff + (unit & 1) * L::kRaw + r * D * 2 + e * (D / 4) + j * 16);
-        const uint32_t u[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = unpack2<T>(u[k]);
-          x[8 * j + 2 * k] = f.x;
-          x[8 * j + 2 * k + 1] = f.y;
-          top = max3(top, fabsf(f.x), fabsf(f.y));
-        }
+      for (int j = 0; j < V; j += 4) {
+        uint2 q2 = make_uint2(0u, 0u);
+        if (r < R) q2 = lds64(from + j * 2);
+        const float2 f0 = unpack2<T>(q2.x), f1 = unpack2<T>(q2.y);
+        x[j] = f0.x;
+        x[j + 1] = f0.y;
+        x[j + 2] = f1.x;
+        x[j + 3] = f1.y;
+        top = max3(max3(top, fabsf(f0.x), fabsf(f0.y)), fabsf(f1.x), fabsf(f1.y));
       }
 #pragma unroll
-      for (int k = 4; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      for (int k = TPR / 2; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
       // largest entry into [2^14, 2^15); rows of zeros, infinities and NaN as they are
       const int ex = (int)(__float_as_uint(top) >> 23) - 127;
       const float up = top > 0.f && ex < 128 ? pow2i(max(min(14 - ex, 127), -126)) : 1.f;
       if (e == 0) rs[r] = fabsf(p.scale) * kLog2e / up;
       const float f = p.scale < 0.f ? -up : up;
 #pragma unroll
-      for (int j = 0; j < D / 8; j += 2) {
-        const int d = e * (D / 8) + j;
+      for (int j = 0; j < V; j += 2) {
+        const int d = e * V + j;
         const int cc = d / (D / 4), ks = (d % (D / 4)) / 4, pair = (d & 3) >> 1;
-        const uint32_t at = sq + (((mt * KS + ks) * 32 + (r & 7) * 4 + cc) * 16) +
-                            (pair * 2 + ((r >> 3) & 1)) * 4;
+        const uint32_t at = FEW ? sq + (ks * 32 + r * 4 + cc) * 8 + pair * 4
+                                : sq + (((mt * KS + ks) * 32 + (r & 7) * 4 + cc) * 16) +
+                                      (pair * 2 + ((r >> 3) & 1)) * 4;
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack2<__half>(x[j] * f, x[j + 1] * f))
                      : "memory");
       }
@@ -379,19 +422,23 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     if (lane == 0) mbar_arrive(&q_empty[unit & 1]);
     if (!(ok = sync())) break;
 
-    float o[NB][4], m[2], l[2], rf[2];
+    // What a lane holds of the scores and the output: of two rows, g and g + 8 (2c and
+    // 2c + 1 for FEW), the row of number x of four being
+    auto row_of = [](int x) { return FEW ? x & 1 : x >> 1; };
+    constexpr int OB = FEW ? NB / 2 : NB;
+    float o[OB][4], m[2], l[2], rf[2];
     int last[2];  // last token that the row sees
     {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int r = rg * 16 + k * 8 + g;
+        const int r = FEW ? 2 * c + k : rg * 16 + k * 8 + g;
         m[k] = -INFINITY;
         l[k] = 0.f;
         rf[k] = rs[r];
         last[k] = r < R ? w.kv - w.nq + r / p.G : w.kv - 1;
       }
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+      for (int j = 0; j < OB; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
     }
@@ -416,12 +463,18 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       // rows of the stage that hold no token, or a page that is not known (or, behind
       // the last token, was not copied): codes of zero
       const bool edge = t0 + 16 * SUB > w.kv || sc[0].x < 0.f || sc[SUB - 1].x < 0.f;
-      // scores: 16 rows x 16 tokens for each row block and group
-      float sr[2 * SUB][4];
+      // scores: of a group, 16 rows x 16 tokens in two blocks; for FEW, 16 tokens x 8 rows in
+      // one.  Of row k of the lane's two, score j < SC and its token in the group:
+      constexpr int SB = FEW ? SUB : 2 * SUB, SC = FEW ? 2 : 4;
+      float sr[SB][4];
+      auto score = [&](int u, int k, int j) -> float& {
+        return FEW ? sr[u][2 * j + k] : sr[(2 * u + (j >> 1)) % SB][2 * k + (j & 1)];
+      };
+      auto token = [&](int j) { return FEW ? g + 8 * j : (j >> 1) * 8 + 2 * c + (j & 1); };
 #pragma unroll
-        for (int nb = 0; nb < 2 * SUB; ++nb)
+      for (int nb = 0; nb < SB; ++nb)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sr[nb][k] = 0.f;
+        for (int k = 0; k < 4; ++k) sr[nb][k] = 0.f;
       {
         uint32_t kw[2 * SUB][KS];
 #pragma unroll
@@ -446,12 +499,23 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
         }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const uint4 a = lds128(sq + ((rg * KS + ks) * 32 + lane) * 16);
+          if constexpr (FEW) {
+            const uint2 q2 = lds64(sq + (ks * 32 + lane) * 8);
 #pragma unroll
-          for (int nb = 0; nb < 2 * SUB; ++nb) {
-            uint32_t k0, k1;
-            e4m3x4_to_f16x4(kw[nb][ks], k0, k1);
-            mma16816(sr[nb], a, k0, k1);
+            for (int u = 0; u < SUB; ++u) {
+              uint4 a;
+              e4m3x4_to_f16x4(kw[2 * u][ks], a.x, a.z);
+              e4m3x4_to_f16x4(kw[2 * u + 1][ks], a.y, a.w);
+              mma16816(sr[u], a, q2.x, q2.y);
+            }
+          } else {
+            const uint4 a = lds128(sq + ((rg * KS + ks) * 32 + lane) * 16);
+#pragma unroll
+            for (int nb = 0; nb < 2 * SUB; ++nb) {
+              uint32_t k0, k1;
+              e4m3x4_to_f16x4(kw[nb][ks], k0, k1);
+              mma16816(sr[nb], a, k0, k1);
+            }
           }
         }
       }
@@ -465,10 +529,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       }
       if (t0 + 16 * SUB - 1 > w.kv - w.nq) {  // some row does not see some token
 #pragma unroll
-          for (int nb = 0; nb < 2 * SUB; ++nb)
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (t0 + nb * 8 + 2 * c + (k & 1) > last[k >> 1]) sr[nb][k] = -INFINITY;
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < SC; ++j)
+              if (t0 + u * 16 + token(j) > last[k]) score(u, k, j) = -INFINITY;
       }
       uint4 pa[SUB];
       {
@@ -482,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
           for (int u = 0; u < SUB; ++u) {
             // (not zero: a masked score stays at -infinity)
             f[u][k] = fmaxf(rf[k] * sc[u].x, 1.17549435e-38f);
-            const float top = fmaxf(max3(sr[2 * u][2 * k], sr[2 * u][2 * k + 1],
-                                         sr[2 * u + 1][2 * k]), sr[2 * u + 1][2 * k + 1]);
+            float top = fmaxf(score(u, k, 0), score(u, k, 1));
+            if (!FEW) top = max3(top, score(u, k, 2 % SC), score(u, k, 3 % SC));
             mx[k] = u ? fmaxf(mx[k], top * f[u][k]) : top * f[u][k];
           }
           grows |= mx[k] > m[k] + kSlack || (m[k] == -INFINITY && mx[k] > -INFINITY);
@@ -492,8 +558,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
           float a[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+#pragma unroll
+            for (int x = FEW ? 4 : 1; x < (FEW ? 32 : 4); x *= 2)  // the row's other lanes
+              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], x));
             const bool up = mx[k] > m[k];  // of the whole row, once any lane of the warp asks
             a[k] = up ? exp2_fast(m[k] - mx[k]) : 1.f;
             if (up) m[k] = mx[k];
@@ -501,34 +568,37 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
             a[k] *= grow;
           }
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            o[j][0] *= a[0];
-            o[j][1] *= a[0];
-            o[j][2] *= a[1];
-            o[j][3] *= a[1];
-          }
+          for (int j = 0; j < OB; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[j][x] *= a[row_of(x)];
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float off = kShift - (m[k] == -INFINITY ? 0.f : m[k]);
           float sum = 0.f;
 #pragma unroll
-          for (int nb = 0; nb < 2 * SUB; ++nb) {
-            const float vf = sc[nb / 2].y * vinv;
+          for (int u = 0; u < SUB; ++u) {
+            const float vf = sc[u].y * vinv;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float e = exp2_fast(fmaf(sr[nb][2 * k + j], f[nb / 2][k], off));
+            for (int j = 0; j < SC; ++j) {
+              const float e = exp2_fast(fmaf(score(u, k, j), f[u][k], off));
               sum += e;
-              sr[nb][2 * k + j] = e * vf;
+              score(u, k, j) = e * vf;
             }
           }
           l[k] += sum;
         }
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-          const float(&x)[4] = sr[2 * u], (&y)[4] = sr[2 * u + 1];
-          pa[u] = make_uint4(pack2<__half>(x[0], x[1]), pack2<__half>(x[2], x[3]),
-                                 pack2<__half>(y[0], y[1]), pack2<__half>(y[2], y[3]));
+          if constexpr (FEW) {
+            // tokens x rows as the scores lie, rows x tokens as the second operand does
+            pa[u].x = transpose8x8(pack2<__half>(sr[u][0], sr[u][1]));
+            pa[u].y = transpose8x8(pack2<__half>(sr[u][2], sr[u][3]));
+          } else {
+            const float(&x)[4] = sr[2 * u], (&y)[4] = sr[2 * u + 1];
+            pa[u] = make_uint4(pack2<__half>(x[0], x[1]), pack2<__half>(x[2], x[3]),
+                               pack2<__half>(y[0], y[1]), pack2<__half>(y[2], y[3]));
+          }
         }
       }
 #pragma unroll
@@ -567,7 +637,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
           e4m3x4_to_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x5140), b1[0], b1[1]);
           e4m3x4_to_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x7362), b1[2], b1[3]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma16816(o[4 * j + k], pa[u], b0[k], b1[k]);
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (!FEW) mma16816(o[4 * j + k], pa[u], b0[k], b1[k]);
+            else if (k % 2 == 0)
+              mma16816(o[2 * j + k / 2], make_uint4(b0[k], b0[k + 1], b1[k], b1[k + 1]), pa[u].x, pa[u].y);
+          }
         }
       }
     }
@@ -579,22 +653,31 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * L::kRows * (D + kPartStats);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
-      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-      const int r = k * 8 + g;
+#pragma unroll
+      for (int x = FEW ? 4 : 1; x < (FEW ? 32 : 4); x *= 2)
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], x);
+      const int r = FEW ? 2 * c + k : k * 8 + g;
       if (rg * 16 + r >= R) continue;
-      if (c == 0) {
+      if ((FEW ? g : c) == 0) {
         wm[warp * 16 + r] = m[k];
         wl[warp * 16 + r] = l[k];
       }
-      // piece j / 4 of column block 2c + jj: no two lanes of a store on one bank
-      float* at = buf + warp * (L::kBuf / 4) + r * (D + 4) + 2 * c * 4;
+      if constexpr (FEW) {
+        // columns D / 8 g on, D / 8 of them
+        float* at = buf + warp * (L::kBuf / 4) + r * (D + 4) + g * NB;
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj)
+        for (int j = 0; j < OB; j += 2)
+          *reinterpret_cast<float4*>(at + 2 * j) = make_float4(o[j][k], o[j][2 + k], o[j + 1][k], o[j + 1][2 + k]);
+      } else {
+        // piece j / 4 of column block 2c + jj: no two lanes of a store on one bank
+        float* at = buf + warp * (L::kBuf / 4) + r * (D + 4) + 2 * c * 4;
 #pragma unroll
-        for (int j = 0; j < NB; j += 4)
-          *reinterpret_cast<float4*>(at + (j / 4) * (D / NB * 4) + jj * 4) = make_float4(
-              o[j][2 * k + jj], o[j + 1][2 * k + jj], o[j + 2][2 * k + jj], o[j + 3][2 * k + jj]);
+        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+          for (int j = 0; j < OB; j += 4)
+            *reinterpret_cast<float4*>(at + (j / 4) * (D / NB * 4) + jj * 4) = make_float4(
+                o[j][2 * k + jj], o[j + 1][2 * k + jj], o[j + 2][2 * k + jj], o[j + 3][2 * k + jj]);
+      }
     }
     if (lane == 0) wv[warp] = vref;
     if (!(ok = sync())) break;
@@ -614,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       for (int k = 0; k < PARTS; ++k) {
         const float a = exp2_fast(wm[(first + k) * 16 + r] - ref), b = a * (wv[first + k] * vdiv);
         const float4 x = *reinterpret_cast<const float4*>(
-            buf + (first + k) * (L::kBuf / 4) + r * (D + 4) + (d4 % (NB / 4)) * (D / NB * 4) +
-            d4 / (NB / 4) * 4);
+            buf + (first + k) * (L::kBuf / 4) + r * (D + 4) +
+            (FEW ? d4 * 4 : (d4 % (NB / 4)) * (D / NB * 4) + d4 / (NB / 4) * 4));
         sum += wl[(first + k) * 16 + r] * a;
         z = make_float4(z.x + x.x * b, z.y + x.y * b, z.z + x.z * b, z.w + x.w * b);
       }
@@ -643,22 +726,23 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
   griddep_launch_dependents();
 }
 
-template <typename T, int D, int RG>
+template <typename T, int D, int ROWS>
 cudaError_t launch_typed(const AttendParams& p, const CUtensorMap& k, const CUtensorMap& v, int box,
                          int ctas, bool whole, cudaStream_t stream) {
-  constexpr int bytes = TokenLayout<D, RG>::kBytes;
+  constexpr int bytes = TokenLayout<D, ROWS>::kBytes;
   static_assert(bytes <= (D == 128 ? 113 : 75) * 1024, "two or three blocks for each SM");
-  const cudaError_t e = allow_shared<token_kernel<T, D, RG>>(bytes);
+  const cudaError_t e = allow_shared<token_kernel<T, D, ROWS>>(bytes);
   if (e != cudaSuccess) return e;
-  token_kernel<T, D, RG><<<ctas, kThreads, bytes, stream>>>(k, v, p, box, whole);
+  token_kernel<T, D, ROWS><<<ctas, kThreads, bytes, stream>>>(k, v, p, box, whole);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_rows(const AttendParams& p, const CUtensorMap& k, const CUtensorMap& v, int box,
                         int rows, int ctas, bool whole, cudaStream_t stream) {
-  return rows <= 16 ? launch_typed<T, D, 1>(p, k, v, box, ctas, whole, stream)
-                    : launch_typed<T, D, 2>(p, k, v, box, ctas, whole, stream);
+  return rows == 8    ? launch_typed<T, D, 8>(p, k, v, box, ctas, whole, stream)
+         : rows == 16 ? launch_typed<T, D, 16>(p, k, v, box, ctas, whole, stream)
+                      : launch_typed<T, D, 32>(p, k, v, box, ctas, whole, stream);
 }
 
 }  // namespace
