@@ -364,6 +364,10 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
   }
 
   // -------------------------------------------------------------- products
+  // r / G for a row r < 32, G <= 32: the error of 2^16 / G, at most 1, times r stays
+  // below 2^16 / G
+  const int per_g = 65536 / p.G + 1;
+  auto token_of = [&](int r) { return r * per_g >> 16; };
   const int g = lane >> 2, c = lane & 3, rg = RG == 2 ? warp >> 1 : 0;
   const uint32_t sq = base + L::kQOff;
   // plain loads: the compiler places them, behind the waits that order them
@@ -404,9 +408,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       for (int k = TPR / 2; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
       // largest entry into [2^14, 2^15); rows of zeros, infinities and NaN as they are
       const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-      const float up = top > 0.f && ex < 128 ? pow2i(max(min(14 - ex, 127), -126)) : 1.f;
-      if (e == 0) rs[r] = fabsf(p.scale) * kLog2e / up;
-      const float f = p.scale < 0.f ? -up : up;
+      const int up = top > 0.f && ex < 128 ? min(14 - ex, 126) : 0;
+      if (e == 0) rs[r] = fabsf(p.scale) * kLog2e * pow2i(-up);
+      const float f = p.scale < 0.f ? -pow2i(up) : pow2i(up);
 #pragma unroll
       for (int j = 0; j < V; j += 2) {
         const int d = e * V + j;
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
         m[k] = -INFINITY;
         l[k] = 0.f;
         rf[k] = rs[r];
-        last[k] = r < R ? w.kv - w.nq + r / p.G : w.kv - 1;
+        last[k] = r < R ? w.kv - w.nq + token_of(r) : w.kv - 1;
       }
 #pragma unroll
       for (int j = 0; j < OB; ++j)
@@ -703,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
         z = make_float4(z.x + x.x * b, z.y + x.y * b, z.z + x.z * b, z.w + x.w * b);
       }
       if (begins && ends) {
-        const int i = rr / p.G, head = w.h * p.G + rr % p.G;
+        const int i = token_of(rr), head = w.h * p.G + rr - i * p.G;
         const int64_t row = ((int64_t)w.b * p.Hq + head) * p.N + i;
         const float inv = sum != 0.f ? 1.f / sum : 0.f;
         uint2 out;
