@@ -165,9 +165,10 @@ __device__ __forceinline__ bool attend_lengths_ok(int64_t kv, int64_t nq, const 
 //   part: rows x d fp32 sums (relative to the row's maximum m and to the largest
 //   scale v of the values), then for each row {m, l, v, 0}, m in log2 units
 constexpr int kPartStats = 4;
-// In tiles: about 5000 cycles against 1200 (tokens), 18000 against 4300 (prompts).
+// In tiles: 3500 to 4000 cycles against 1000 (tokens), 18000 against 4300 (prompts).
 // Without it blocks whose share is many short units ended last (3 prompts of 2510
-// tokens, 32 heads in groups of eight: 368 us instead of 231).
+// tokens, 32 heads in groups of eight: 368 us; with 2, 4 and 6: 261, 230 and 238; token
+// calls differ by 2% between these).
 constexpr int kUnitCost = 4;
 
 // A block's place on the line: place `x` of a unit of `tiles` tiles, `left` places from

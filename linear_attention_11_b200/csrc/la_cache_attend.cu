@@ -11,7 +11,7 @@ namespace {
 constexpr int kTokenRows = 32;
 // Short sequences leave their units whole: no line to find one's place on, no parts,
 // no workspace, one launch.  Token calls whose page tables hold at most kWholeTokens
-// tokens a sequence (16 heads, 333 tokens: 8.2 us instead of 9.4, and 12 us instead of 16
+// tokens a sequence (16 heads, 333 tokens: 7.5 us instead of 10.7, and 12 us instead of 16
 // of the host's time); prompts whose tables hold at most kWholePrompt, or kWholePrompts
 // with a unit for every SM (9 prompts of 49 tokens, 4 heads: 14 us instead of 27).
 constexpr int kWholeTokens = 512, kWholePrompt = 512, kWholePrompts = 1024;

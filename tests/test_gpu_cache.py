@@ -189,6 +189,30 @@ def test_tokens(la, G, d, page, dtype, N):
     attend_both(la, cache, table, q, kv, nq, what=f"{G} {d} {page} {dtype} {N}")
 
 
+@pytest.mark.parametrize("G,N", [(1, 7), (2, 4), (8, 1), (9, 1), (3, 3), (1, 16), (17, 1), (1, 32), (1, 33)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_numbers_of_rows(la, G, N, d):
+    """Around 8, 16 and 32 rows, over tables that leave units whole and that do not; one row is NaN and
+    changes no other."""
+    kv, nq = [N + 140, N, 3, 610], [N, N, min(N, 3), max(1, N - 1)]
+    cache, table = filled_cache(kv, 2, 32, d, G + N)
+    wide = np.full((4, 300), -1, dtype=np.int32)
+    wide[:, :table.shape[1]] = table
+    q = normal(N, 4, 2 * G, N, d).half()
+    lost = q.clone()
+    lost[0, G, 0, d // 2] = float("nan")
+    scale = -0.3 if d == 64 else d ** -0.5
+    ref = oc.attend(cache, table, q.double().numpy(), kv, nq, scale)
+    for t in (table, wide):
+        attend_both(la, cache, t, q, kv, nq, scale=scale)
+        got = torch.zeros_like(q, device=DEV)
+        la.la_cache_attend(lost.to(DEV), to_device(la, cache, DEV), torch.from_numpy(t).to(DEV), ints(kv, DEV),
+                           q_len=ints(nq, DEV), o=got, scale=scale)
+        assert got[0, G, 0].isnan().all()
+        got[0, G, 0] = torch.from_numpy(ref[0][0, G, 0]).half()
+        assert_attend(got, None, ref, max(kv), d, q.dtype)
+
+
 @pytest.mark.parametrize("G,d,page,dtype", SHAPES)
 @pytest.mark.parametrize("N,past", [(40, [0, 3, 100, 129]), (130, [0, 1, 64, 250]), (300, [0, 20])])
 def test_prompts(la, G, d, page, dtype, N, past):
