@@ -479,6 +479,26 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       for (int nb = 0; nb < SB; ++nb)
 #pragma unroll
         for (int k = 0; k < 4; ++k) sr[nb][k] = 0.f;
+      // values: of a group tokens 2c, 2c + 1, 2c + 8, 2c + 9, D / 8 numbers each from
+      // (D / 8) g on
+      uint32_t vw[FEW ? SUB : 1][4][D / 32];
+      auto load_values = [&](int u, uint32_t (&x)[4][D / 32]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = u * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 y = lds128(vb + row * D + ((g ^ (row & 7)) << 4));
+            x[k][0] = y.x; x[k][1] = y.y; x[k][2] = y.z; x[k][3] = y.w;
+          } else {
+            const uint2 y = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+            x[k][0] = y.x; x[k][1] = y.y;
+          }
+        }
+      };
+      auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+      };
       {
         uint32_t kw[2 * SUB][KS];
 #pragma unroll
@@ -522,6 +542,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
             }
           }
         }
+      }
+      if constexpr (FEW) {  // there are registers for the values: the stage is free at once
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) load_values(u, vw[u]);
+        release();
       }
       // value scales: a larger one than before makes the sums relative to it
       float grow = 1.f;
@@ -607,39 +632,24 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
       }
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        // values: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of the group, D / 8 numbers each
-        // from (D / 8) g on
-        uint32_t vw[4][D / 32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = u * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
-          if constexpr (D == 128) {
-            const uint4 x = lds128(vb + row * D + ((g ^ (row & 7)) << 4));
-            vw[k][0] = x.x; vw[k][1] = x.y; vw[k][2] = x.z; vw[k][3] = x.w;
-          } else {
-            const uint2 x = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-            vw[k][0] = x.x; vw[k][1] = x.y;
-          }
-        }
+        uint32_t (&v)[4][D / 32] = vw[FEW ? u : 0];
+        if constexpr (!FEW) load_values(u, v);
         if (edge) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (sc[u].x < 0.f || t0 + u * 16 + 2 * c + (k & 1) + (k >> 1) * 8 >= w.kv)
 #pragma unroll
-              for (int j = 0; j < D / 32; ++j) vw[k][j] = 0u;
+              for (int j = 0; j < D / 32; ++j) v[k][j] = 0u;
         }
-        if (u == SUB - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[s]);
-        }
+        if (!FEW && u == SUB - 1) release();
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           // two tokens' bytes of a number side by side
           uint32_t b0[4], b1[4];
-          e4m3x4_to_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x5140), b0[0], b0[1]);
-          e4m3x4_to_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x7362), b0[2], b0[3]);
-          e4m3x4_to_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x5140), b1[0], b1[1]);
-          e4m3x4_to_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x7362), b1[2], b1[3]);
+          e4m3x4_to_f16x4(__byte_perm(v[0][j], v[1][j], 0x5140), b0[0], b0[1]);
+          e4m3x4_to_f16x4(__byte_perm(v[0][j], v[1][j], 0x7362), b0[2], b0[3]);
+          e4m3x4_to_f16x4(__byte_perm(v[2][j], v[3][j], 0x5140), b1[0], b1[1]);
+          e4m3x4_to_f16x4(__byte_perm(v[2][j], v[3][j], 0x7362), b1[2], b1[3]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if constexpr (!FEW) mma16816(o[4 * j + k], pa[u], b0[k], b1[k]);
