@@ -25,7 +25,9 @@
 //   O^T = V^T P^T: half the products, exponentials and sums of the other way round
 //   (more rows are its 16-wide side).  Weights come out of the first as tokens x rows
 //   and are turned by movmatrix.  256 sequences, groups of four: 231 us the other
-//   way, 206 this; a million tokens, 8 heads, one row each: 334 and 320.
+//   way, 206 this; a million tokens, 8 heads, one row each: 334 and 320 (198 and 314 with
+//   the values loaded before the softmax, which leaves the stage free half a step
+//   earlier).
 // - q is scaled by a power of two for each row so that its largest entry lies in
 //   [2^14, 2^15) before it is rounded to f16: exact down to 2^-28 of the largest.
 // - Weights go to f16 as 2^7 p b_j / v, v the largest value scale so far (a power
