@@ -196,6 +196,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// Adds x >= 0, a step's own sum, to a row's sum l >= 0.  What the addition rounds off
+// is kept in `lost`, to be added at the end: a step far below half a place of l (a key with
+// most of the weight, then 2^18 of 2^-24.5 of it) would leave no trace otherwise.  Off by 2^-23 x
+// at most also where x > l.
+__device__ __forceinline__ void add_up(float& l, float& lost, float x) {
+  const float sum = l + x;
+  lost += x - (sum - l);
+  l = sum;
+}
+
 // Weights are held as 2^kAttendShift at a row's reference maximum.
 constexpr float kAttendShift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;

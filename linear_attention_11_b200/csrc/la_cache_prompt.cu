@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       }
       f = fmaxf(f * ek, 1.17549435e-38f);  // not zero: a masked score stays at -infinity
 
-      float m = -INFINITY, l = 0.f;  // reference maximum, sum of weights
+      float m = -INFINITY, l = 0.f, lost = 0.f;  // reference maximum, sum of weights, see add_up
       for (int i = 0; i < mine; ++i, ++it) {
         ok = warp_wait_brief(&s_full[t], it & 1, abort_flag);
         if (!ok) break;
@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           const float a = grows ? exp2_fast(m - mt) : 1.f;
           if (grows) m = mt;
           l *= a;
+          lost *= a;
           if (i > 0) {  // the product of the tile before is in: it was issued before these scores
 #pragma unroll 1
             for (int k = 0; k < D / 16; ++k) {
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         }
         const float off = kShift - (m == -INFINITY ? 0.f : m);
         const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-        float2 sum = make_float2(l, 0.f), sum2 = make_float2(0.f, 0.f);
+        float2 sum = make_float2(0.f, 0.f), sum2 = sum;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           scores(half, x);
@@ -480,8 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
         }
         sum = add2(sum, sum2);
-        l = sum.x + sum.y;
+        add_up(l, lost, sum.x + sum.y);
       }
+      l += lost;
       if (!ok) break;
 
       // the unit's output, or its part

@@ -432,14 +432,14 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     // 2c + 1 for FEW), the row of number x of four being
     auto row_of = [](int x) { return FEW ? x & 1 : x >> 1; };
     constexpr int OB = FEW ? NB / 2 : NB;
-    float o[OB][4], m[2], l[2], rf[2];
+    float o[OB][4], m[2], l[2], lost[2], rf[2];
     int last[2];  // last token that the row sees
     {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = FEW ? 2 * c + k : rg * 16 + k * 8 + g;
         m[k] = -INFINITY;
-        l[k] = 0.f;
+        l[k] = lost[k] = 0.f;
         rf[k] = rs[r];
         last[k] = r < R ? w.kv - w.nq + token_of(r) : w.kv - 1;
       }
@@ -596,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
             a[k] = up ? exp2_fast(m[k] - mx[k]) : 1.f;
             if (up) m[k] = mx[k];
             l[k] *= a[k];
+            lost[k] *= a[k];
             a[k] *= grow;
           }
 #pragma unroll
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
               score(u, k, j) = e * vf;
             }
           }
-          l[k] += sum;
+          add_up(l[k], lost[k], sum);
         }
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * L::kRows * (D + kPartStats);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+      l[k] += lost[k];
 #pragma unroll
       for (int x = FEW ? 4 : 1; x < (FEW ? 32 : 4); x *= 2)
         l[k] += __shfl_xor_sync(0xffffffffu, l[k], x);
