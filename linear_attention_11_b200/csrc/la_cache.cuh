@@ -182,6 +182,9 @@ struct Place {
   }
 };
 
+// Tokens of a page table over which prompts' units may be left whole, at most.
+constexpr int kWholePrompts = 1024;
+
 // tails[block] = {blocks that hold the rest (0: nothing to join), b, kv head, query tile}
 
 // A unit's rows: `rows` in `blocks` tiles of tile_rows, the first

@@ -14,7 +14,8 @@ constexpr int kTokenRows = 32;
 // tokens a sequence (16 heads, 333 tokens: 7.5 us instead of 10.7, and 12 us instead of 16
 // of the host's time); prompts whose tables hold at most kWholePrompt, or kWholePrompts
 // with a unit for every SM (9 prompts of 49 tokens, 4 heads: 14 us instead of 27).
-constexpr int kWholeTokens = 512, kWholePrompt = 512, kWholePrompts = 1024;
+constexpr int kWholeTokens = 512, kWholePrompt = 512;
+static_assert(kWholePrompt <= kWholePrompts, "the most");
 
 struct Shape {
   bool token, whole;

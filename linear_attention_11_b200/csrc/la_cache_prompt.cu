@@ -43,6 +43,13 @@ constexpr int kIssue = 16, kPlan = 17;  // the warps that issue products and pla
 constexpr int kPlans = 4;               // units that the plan is ahead at most
 constexpr float kShift = kAttendShift;
 constexpr float kSlack = 8.f;  // growth of a row's maximum that is let pass
+// Key tiles whose products O takes up in tensor memory; then it is added to its part in
+// the workspace and begins again.  The products cut off what lies below the sum's last
+// places and do not round it: over 2^18 tokens in one sum, all values 1, o was 0.9937.
+// 1024 tokens over 32768: 2.23 ms without, 2.25 with 128 tiles, 2.30 with 64.
+constexpr int kChain = 128;
+static_assert((kChain & (kChain - 1)) == 0, "a power of two");
+static_assert(kChain * kKeys >= kWholePrompts, "whole units have no workspace");
 // Registers of a thread after the split; 640 x 96 at launch.  With 40 for the issuing
 // warp its descriptors go through local memory: 1.36 ms instead of 1.26 for four
 // prompts of 8192 tokens and 16 heads.
@@ -170,6 +177,12 @@ __device__ __forceinline__ int load_word(const int* p, bool there, int other) {
       : "=&r"(v)
       : "l"(p), "r"((uint32_t)there), "r"(other));
   return v;
+}
+
+// a z + x, four fp32 numbers of x as they come from tensor memory.
+__device__ __forceinline__ float4 plus(const float4& z, float a, const uint32_t* x) {
+  return make_float4(fmaf(z.x, a, __uint_as_float(x[0])), fmaf(z.y, a, __uint_as_float(x[1])),
+                     fmaf(z.z, a, __uint_as_float(x[2])), fmaf(z.w, a, __uint_as_float(x[3])));
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 f) {
@@ -409,79 +422,117 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       }
       f = fmaxf(f * ek, 1.17549435e-38f);  // not zero: a masked score stays at -infinity
 
+      // The block's part of the unit in the workspace.  Of a unit that is not cut its sums
+      // lie where those of the share's last unit will, which comes later.
+      auto part_at = [&]() {
+        return p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * 256 * (D + kPartStats);
+      };
+      // Four sums of this thread's row, columns c * 32 + 4 k on: in those columns of the warp's
+      // rows, whole lines for each k.
+      auto sums_at = [&](int c, int k) {
+        const int r = t * 128 + (warp & 3) * 32 + k * 4 + (lane >> 3);
+        return reinterpret_cast<float4*>(part_at() + (int64_t)r * D + c * 32) + (lane & 7);
+      };
+      auto part_stats = [&]() { return part_at() + 256 * D + (t * 128 + rr) * kPartStats; };
+
       float m = -INFINITY, l = 0.f, lost = 0.f;  // reference maximum, sum of weights, see add_up
-      for (int i = 0; i < mine; ++i, ++it) {
-        ok = warp_wait_brief(&s_full[t], it & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const int sees = last - first - i * kKeys;  // columns up to this one are seen
-        const bool masked = __any_sync(0xffffffffu, sees < kKeys - 1);
-        // The row goes by twice, 64 scores at a time: held whole it would take the
-        // registers that the conversion needs.
-        auto scores = [&](int half, uint32_t (&x)[64]) {
-          tmem_ld32(st + half * 64, *reinterpret_cast<uint32_t(*)[32]>(x));
-          tmem_ld32(st + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
-          tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-              if (half * 64 + k > sees) x[k] = __float_as_uint(-INFINITY);
-          }
-        };
-        uint32_t x[64];
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          scores(half, x);
-#pragma unroll
-          for (int k = 0; k < 64; k += 2)
-            top[(k >> 1) & 3] = max3(top[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-        }
-        top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        const float mt = top[0] == -INFINITY ? -INFINITY : top[0] * f;
-        const bool grows = mt > m + kSlack || (m == -INFINITY && mt > -INFINITY);
-        if (__any_sync(0xffffffffu, grows)) {
-          // a new reference: the sum so far and O go by 2^(old - new)
-          const float a = grows ? exp2_fast(m - mt) : 1.f;
-          if (grows) m = mt;
-          l *= a;
-          lost *= a;
-          if (i > 0) {  // the product of the tile before is in: it was issued before these scores
+      for (int i0 = 0; i0 < mine && ok; i0 += kChain) {
+        if (i0 > 0) {
+          // O, all products before these scores, to the row's sums so far; those are relative
+          // to 2^(their m)
+          ok = warp_wait_brief(&s_full[t], it & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const float a = i0 > kChain && m > -INFINITY ? exp2_fast(*part_stats() - m) : 0.f;
 #pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t y[16];
-              tmem_ld16(ot + k * 16, y);
-              tmem_wait_ld();
+          for (int c = 0; c < D / 32; ++c) {
+            float4 z[8];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a);
-              tmem_st16(ot + k * 16, y);
+            for (int k = 0; k < 8; ++k)
+              z[k] = i0 > kChain ? *sums_at(c, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+            uint32_t y[32];
+            tmem_ld32(ot + c * 32, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *sums_at(c, k) = plus(z[k], a, y + 4 * k);
+          }
+          *part_stats() = m;
+        }
+#pragma unroll 1
+        for (int i = i0; i < min(mine, i0 + kChain); ++i, ++it) {
+          ok = warp_wait_brief(&s_full[t], it & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const int sees = last - first - i * kKeys;  // columns up to this one are seen
+          const bool masked = __any_sync(0xffffffffu, sees < kKeys - 1);
+          // The row goes by twice, 64 scores at a time: held whole it would take the
+          // registers that the conversion needs.
+          auto scores = [&](int half, uint32_t (&x)[64]) {
+            tmem_ld32(st + half * 64, *reinterpret_cast<uint32_t(*)[32]>(x));
+            tmem_ld32(st + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+            tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int k = 0; k < 64; ++k)
+                if (half * 64 + k > sees) x[k] = __float_as_uint(-INFINITY);
+            }
+          };
+          uint32_t x[64];
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            scores(half, x);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2)
+              top[(k >> 1) & 3] = max3(top[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+          }
+          top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+          const float mt = top[0] == -INFINITY ? -INFINITY : top[0] * f;
+          const bool grows = mt > m + kSlack || (m == -INFINITY && mt > -INFINITY);
+          if (__any_sync(0xffffffffu, grows)) {
+            // a new reference: the sum so far and O go by 2^(old - new)
+            const float a = grows ? exp2_fast(m - mt) : 1.f;
+            if (grows) m = mt;
+            l *= a;
+            lost *= a;
+            if (i > i0) {  // the product of the tile before is in: it was issued before these scores
+#pragma unroll 1
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t y[16];
+                tmem_ld16(ot + k * 16, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a);
+                tmem_st16(ot + k * 16, y);
+              }
             }
           }
-        }
-        const float off = kShift - (m == -INFINITY ? 0.f : m);
-        const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-        float2 sum = make_float2(0.f, 0.f), sum2 = sum;
+          const float off = kShift - (m == -INFINITY ? 0.f : m);
+          const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+          float2 sum = make_float2(0.f, 0.f), sum2 = sum;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          scores(half, x);
-          uint32_t y[32];
+          for (int half = 0; half < 2; ++half) {
+            scores(half, x);
+            uint32_t y[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float2 w = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, off2);
-            w.x = exp2_fast(w.x);
-            w.y = exp2_fast(w.y);
-            if (k & 1) sum2 = add2(sum2, w);
-            else sum = add2(sum, w);
-            y[k] = pack2<__half>(w.x, w.y);
+            for (int k = 0; k < 32; ++k) {
+              float2 w = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, off2);
+              w.x = exp2_fast(w.x);
+              w.y = exp2_fast(w.y);
+              if (k & 1) sum2 = add2(sum2, w);
+              else sum = add2(sum, w);
+              y[k] = pack2<__half>(w.x, w.y);
+            }
+            tmem_st32(st + half * 32, y);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
           }
-          tmem_st32(st + half * 32, y);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+          sum = add2(sum, sum2);
+          add_up(l, lost, sum.x + sum.y);
         }
-        sum = add2(sum, sum2);
-        add_up(l, lost, sum.x + sum.y);
       }
       l += lost;
       if (!ok) break;
@@ -493,7 +544,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         if (!ok) break;
         tc_fence_after();
       }
-      float* part = p.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * 256 * (D + kPartStats);
+      float* part = part_at();
+      const bool chained = mine > kChain;  // O holds what came behind the sums in the workspace
+      const float before = chained && m > -INFINITY ? exp2_fast(*part_stats() - m) : 0.f;
       // Rows go out through the warp's part of the q tile, which its products have
       // read, so that a store covers whole rows.
       const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -503,6 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         if (mine > 0) {
           tmem_ld32(ot + c * 32, x);
           tmem_wait_ld();
+          if (chained) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 z = plus(*sums_at(c, k >> 2), before, x + k);
+              x[k] = __float_as_uint(z.x);
+              x[k + 1] = __float_as_uint(z.y);
+              x[k + 2] = __float_as_uint(z.z);
+              x[k + 3] = __float_as_uint(z.w);
+            }
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = 0u;
@@ -555,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       if (valid && whole) {
         if (p.lse) p.lse[row] = (m - kShift + log2f(l)) * kLn2;
       } else if (valid) {
-        reinterpret_cast<float4*>(part + 256 * D)[t * 128 + rr] = make_float4(m, l, ev, 0.f);
+        *reinterpret_cast<float4*>(part_stats()) = make_float4(m, l, ev, 0.f);
       }
     }
   } else if (warp < kIssue) {
@@ -734,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
 #pragma unroll
               for (int kk = 4 * h; kk < 4 * h + 4; ++kk)  // O += P V
                 mma_ts(pt + 256, pt + kk * 8, smem_desc_sw128(vt + kk * 2048, kKeys * 128, 1024),
-                       IDESC_PV, i > 0 || kk > 0 ? 1u : 0u);
+                       IDESC_PV, (i & (kChain - 1)) != 0 || kk > 0 ? 1u : 0u);
             }
             if (!ok) break;
             p_parity ^= 1u << t;

@@ -18,7 +18,7 @@ import torch
 
 from oracle import cache as oc
 
-from _cache_cases import ints, to_device
+from _cache_cases import filled_cache, ints, normal, to_device
 
 pytestmark = pytest.mark.gpu
 
@@ -69,12 +69,21 @@ def check(la, cache, table, q, scale, kv=None):
     o = la.la_cache_attend(x, to_device(la, cache, DEV), torch.from_numpy(table).to(DEV), ints([kv] * B, DEV),
                            lse=lse, scale=scale)
     assert la.la_device_status() == (0, 0)
-    assert torch.isfinite(o).all()
-    lse = lse.double().cpu().numpy()
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    half = torch.finfo(q.dtype).eps / 2
     for g in range(G):
-        _, want_lse, _, lse_tol = attend_pages(cache, table[0], q[g].double().numpy(), kv, scale, cut_off(G * N))
+        want, want_lse, o_tol, lse_tol = attend_pages(cache, table[0], q[g].double().numpy(), kv, scale,
+                                                      cut_off(G * N))
         off = np.abs(lse[:, g] - want_lse) / lse_tol
         assert off.max() <= 1, f"lse {off.max():.2f} of the bound"
+        off = np.abs(o[:, g] - want) / (o_tol * (1 + half) + half * np.abs(want))
+        assert off.max() <= 1, f"o {off.max():.2f} of the bound, {np.abs(o[:, g] - want).max():.2e}"
+
+
+def some_pages(count, d, seed):
+    """A cache of `count` full pages."""
+    cache, table = filled_cache([count * PAGE], 1, PAGE, d, seed)
+    return {n: a[table[0]] for n, a in cache.items()}
 
 
 SHAPES = [(1, 1, 64), (4, 4, 64), (4, 8, 128), (1, 40, 64), (1, 40, 128), (2, 200, 64)]   # G, N, d
@@ -83,7 +92,7 @@ SHAPES = [(1, 1, 64), (4, 4, 64), (4, 8, 128), (1, 40, 64), (1, 40, 128), (2, 20
 @pytest.mark.parametrize("G,N,d", SHAPES)
 @pytest.mark.parametrize("log_n,gap", [(20, 20.3), (18, 24.5), (20, 24.5), (20, 0.585)])
 def test_a_large_weight_and_a_million_small_ones(la, G, N, d, log_n, gap):
-    """One key 2^gap above all others, every value 1: lse tells the others' share.  More
+    """One key 2^gap above all others, every value 1: o is 1 and lse tells the others' share.  More
     sequences than blocks, so that each sequence is one block's."""
     B = 300 if G * N <= 32 else 160
     cache = {n: np.zeros((2, 1, PAGE, d), np.uint8) for n in "kv"}
@@ -93,3 +102,30 @@ def test_a_large_weight_and_a_million_small_ones(la, G, N, d, log_n, gap):
     table = np.ones((B, 2 ** log_n // PAGE), dtype=np.int32)
     table[:, 0] = 0
     check(la, cache, table, torch.ones(G, N, d).half(), gap * math.log(2) / d)
+
+
+@pytest.mark.parametrize("G,N,d", SHAPES)
+@pytest.mark.parametrize("B,log_n", [(1, 23), (3, 20)])
+def test_long_sequences_split_over_the_gpu(la, G, N, d, B, log_n):
+    """Chains that end inside a block's share, of units cut between blocks and of whole ones; a length
+    that ends inside a page."""
+    cache = some_pages(5, d, G + N)
+    table = np.random.default_rng(N).integers(0, 5, (1, 2 ** log_n // PAGE)).astype(np.int32).repeat(B, 0)
+    check(la, cache, table, (normal(N, G, N, d) * 1.5).half(), d ** -0.5, kv=2 ** log_n - 77)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_maximum_that_grows_from_chain_to_chain(la, dtype):
+    """Scores that rise by 2^10 and more along the sequence, so that the sums put by are relative to
+    smaller maxima than those that follow, and values whose scales grow too."""
+    d, parts = 64, 6
+    cache = some_pages(parts, d, 3)
+    per = 300                      # pages of a kind in a row: more than two chains of prompts, nine of tokens
+    table = np.repeat(np.arange(parts), per).astype(np.int32)[None].repeat(160, 0)
+    for p in range(parts):
+        cache["v_scale"][p] *= 2.0 ** (2 * p)
+        cache["k"][p, 0, :, 0] = oc.round_e4m3(np.full(PAGE, p / 8) / cache["k_scale"][p, 0])
+    for G, N in ((1, 1), (4, 8), (1, 64)):
+        q = normal(N, G, N, d)
+        q[..., 0] = 400.0          # 400 / 8 * d ** -0.5: 2^9 from each kind to the next
+        check(la, cache, table, q.to(dtype), d ** -0.5)
