@@ -382,12 +382,16 @@ la_status la_cache_read(const la_cache *cache, const int32_t *table, const int32
  *   q, o      bf16 or fp16 [B,Hq,N,d], o not overlapping q or the cache
  *   lse       fp32 [B,Hq,N], or null
  *   scale     finite; usually 1/sqrt(d)
- * Scores, the softmax's sums and the products' sums are held in fp32; weights, and
- * codes times scales, enter the products as fp16, relative to the largest weight of
- * the row and the largest scale among the sequence's pages of the head.  A page whose
- * scale is 2^-15 of that or more counts exactly, a smaller one to 2^-25 of it (a row
- * that sees only such pages keeps no more of them), a weight to 2^-32 of the row's
- * largest.
+ * Scores, the softmax's sums and the products' sums are held in fp32.  Weights enter the
+ * product with the values as fp16, 2^-11 of each or, of the small ones, 2^-32 of the row's
+ * largest.  Scales go with them or with the codes:
+ *   up to 32 rows for each kv head   a weight is rounded times its page's scale of the values: to
+ *             2^-32 of the row's largest weight times the largest scale of the sequence's pages
+ *   more rows   codes are, times their page's scale: exact in pages whose scale is 2^-22 or more
+ *             of the largest one among the pages that a group of 256 rows sees; in others each
+ *             value is off by 2^-32 of that at most
+ * So values far below others keep fewer bits, for all rows of the group: also for its early
+ * rows that see only the small ones.
  * Splits long sequences over the SMs and joins the parts; the parts' workspace
  * comes from the stream-ordered pool (la_cache_attend) or from the caller
  * (la_cache_attend_ws: 256-byte aligned, at least

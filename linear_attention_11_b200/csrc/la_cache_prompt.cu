@@ -21,9 +21,10 @@
 //   warp 17         goes ahead from unit to unit and writes down for the others what
 //                   they are (18 and 19 fill up the warpgroup: registers go by those)
 // The scale of a page against the largest of the block's share of the unit is a
-// power of two and goes into the conversion (exact in f16 down to 2^-15 of the
-// largest; below, codes lose bits that weigh 2^-24 of it), so one factor a row is
-// left for the scores and one a unit for the output.
+// power of two and goes into the conversion, so one factor a row is left for the scores
+// and one a unit for the output.  Exact in f16 down to 2^-15 of the largest.  Where a
+// page is smaller, the unit's factors are 2^7 (448 x 2^7 still is an f16): exact down to
+// 2^-22, and below that values lose what is under 2^-32 of the largest scale.
 // P (f16) is written over its scores; O stays in tensor memory, and is rescaled
 // only when a row's maximum grows by more than 2^8: weights are 2^7 at a row's
 // reference maximum and stay below 2^15, and count down to 2^-32 of it.
@@ -64,7 +65,7 @@ struct Unit {
   int kv, nq;
   int begins, ends;  // whether the unit's first and last tiles are among them
   int follow;        // of a unit that begins but does not end: blocks that hold the rest
-  float ek, ev;      // largest scales of the pages
+  float ek, ev;      // what codes are scaled against: the pages' largest scales, or 2^-7 of them
 };
 
 template <int D>
@@ -675,14 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
                             at >= 0 && first + i * kKeys + r < kv);
         }
       };
+      // (the factor as a product of two: one of 2^-14 or more leaves every code exact, so
+      // a second one rounds once)
       auto store = [&](const uint4 (&x)[kLoads], float factor, int slot) {
         const uint32_t dst = base + L::kSlotOff + slot * L::kSlot + store_at;
-        const __half2 fh = __float2half2_rn(factor);
-        const uint32_t fw = *reinterpret_cast<const uint32_t*>(&fh);
+        const uint32_t fw = pack2<__half>(fmaxf(factor, 0x1p-14f), fminf(factor * 0x1p14f, 1.f));
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
           const uint32_t fj = __shfl_sync(0xffffffffu, fw, (j * kRowsPerLoad + sub) >> 4);
-          const __half2 f2 = *reinterpret_cast<const __half2*>(&fj);
           const bool one = fj == 0x3c003c00u;  // as for most pages: no product needed
           const uint32_t c[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
           uint32_t y[8];
@@ -694,8 +695,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
             y[2 * k + 1] = hi;
           }
           if (!one) {
+            const __half2 f2 = *reinterpret_cast<const __half2*>(&fj);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = hmul2(y[k], f2);
+            for (int k = 0; k < 8; ++k) y[k] = hmul2(y[k], __low2half2(f2));
+            if (fj >> 16 != 0x3c00u) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = hmul2(y[k], __high2half2(f2));
+            }
           }
           st_shared_v4(dst + j * (kRowsPerLoad * 128), y[0], y[1], y[2], y[3]);
           st_shared_v4((dst ^ 16) + j * (kRowsPerLoad * 128), y[4], y[5], y[6], y[7]);
@@ -824,7 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         const bool more = w.pos < w.end;
         float ek = 0.f, ev = 0.f;
         if (more) {
-          // the largest scales among the pages of these tiles
+          // the largest scales among the pages of these tiles, and the least
+          float lk = INFINITY, lv = INFINITY;
           const int n = w.count(), c = max(w.count(0, n), w.count(1, n));
           const int t0 = w.tile(), stop = min(w.kv, (t0 + c) * kKeys);
           const int g1 = stop > t0 * kKeys ? ((stop - 1) >> p.page_log2) + 1 : 0;
@@ -833,8 +840,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           for (int g = ((t0 * kKeys) >> p.page_log2) + lane; g < g1; g += 32) {
             const int id = __ldg(ids + g);
             if (id >= 0 && id < p.num_pages) {
-              ek = fmaxf(ek, __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + w.h));
-              ev = fmaxf(ev, __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + w.h));
+              const float sk = __ldg(p.kvscale[0] + (int64_t)id * p.Hkv + w.h);
+              const float sv = __ldg(p.kvscale[1] + (int64_t)id * p.Hkv + w.h);
+              ek = fmaxf(ek, sk);
+              ev = fmaxf(ev, sv);
+              if (sk > 0.f) lk = fminf(lk, sk);
+              if (sv > 0.f) lv = fminf(lv, sv);
             } else {
               atomicOr(p.status, kDevBadIndex);
             }
@@ -843,7 +854,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           for (int k = 16; k > 0; k >>= 1) {
             ek = fmaxf(ek, __shfl_xor_sync(0xffffffffu, ek, k));
             ev = fmaxf(ev, __shfl_xor_sync(0xffffffffu, ev, k));
+            lk = fminf(lk, __shfl_xor_sync(0xffffffffu, lk, k));
+            lv = fminf(lv, __shfl_xor_sync(0xffffffffu, lv, k));
           }
+          if (lk < ek * 0x1p-15f) ek *= 0x1p-7f;
+          if (lv < ev * 0x1p-15f) ev *= 0x1p-7f;
         }
         if (lane == 0) {
           unit.n = -1;
