@@ -420,9 +420,10 @@ la_status la_cache_attend_ws(const void *q, la_dtype dtype, const la_cache *cach
  * synchronisation reports a fault, else LA_OK.
  *
  * la_selftest_wait: launches one warp that waits, bounded by timeout_ns of
- * device time, on a device flag that nothing ever sets; when the limit passes
- * it records LA_DEV_TIMEOUT and returns.  Exercises the same bounded-wait
- * routine the kernels use, without faulting or hanging the GPU.
+ * device time, on a device flag that nothing ever sets, and then for a few
+ * milliseconds on a barrier that nothing arrives at; when both limits have
+ * passed it records LA_DEV_TIMEOUT and returns.  Exercises the same bounded-wait
+ * routines the kernels use, without faulting or hanging the GPU.
  * ---------------------------------------------------------------------- */
 la_status la_device_status(unsigned int *flags, int clear);
 la_status la_selftest_wait(int64_t timeout_ns, la_stream stream);

@@ -272,15 +272,27 @@ bool make_tmap_state(CUtensorMap* map, const void* base, int64_t units) {
 
 namespace {
 
+// Both bounded waits of the kernels, of one warp: on a flag that nothing sets, by the clock, then
+// on a barrier that nothing arrives at, by tries (4 ms), which ends as a role of a block does.
+// The status bit tells that both have run out.
 __global__ void selftest_wait_kernel(unsigned* status, const unsigned* flag, int64_t limit_ns) {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncwarp();
   const uint64_t t0 = globaltimer_ns();
-  while (*reinterpret_cast<const volatile unsigned*>(flag) == 0u) {
-    if (globaltimer_ns() - t0 > (uint64_t)limit_ns) {
-      if (threadIdx.x == 0) atomicOr(status, kDevTimeout);
-      return;
-    }
+  while (globaltimer_ns() - t0 <= (uint64_t)limit_ns) {
+    if (*reinterpret_cast<const volatile unsigned*>(flag) != 0u) return;
     __nanosleep(1000);
   }
+  volatile int* abort = &abort_flag;
+  if (mbar_wait_brief(&bar, 0, abort, 1000)) return;
+  __syncwarp();
+  if (threadIdx.x == 0) give_up(status, abort);
 }
 
 }  // namespace

@@ -78,7 +78,7 @@ struct PromptLayout {
   static constexpr int kUnitOff = kMiscOff + 23 * 8;  // scan scratch 20 x 8, start 3 x 8
   static constexpr int kBarOff = kUnitOff + kPlans * 64;
   static constexpr int kBars = 2 * kSlots + 2 * 5 + 2 * kPlans + 1;
-  static constexpr int kEnd = kBarOff + kBars * 8 + 16;  // tmem slot, abort flag
+  static constexpr int kEnd = kBarOff + kBars * 8 + 16;  // tmem slot, abort flag, ticks
   static constexpr int kBytes = kEnd + 1024;
 };
 
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   uint64_t* done = u_empty + kPlans;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* ticks = abort_flag + 1;  // tiles converted so far
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
     }
     mbar_init(done, 1);
     *abort_flag = 0;
+    *ticks = 0;
     fence_barrier_init();
   }
   if (warp == kIssue) {
@@ -319,9 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // by a whole warp: unit `seg` once it is written down, and that it has been read
+  // by a whole warp: unit `seg` once it is written down, and that it has been read.  Warps
+  // whose row tile has no rows, and the one that plans, are ahead of the others here, and wait for
+  // as long as a unit takes: with a limit of 2 s one of 2^27 tokens would have been given up.
   auto wait_unit = [&](int seg) {
-    return warp_wait_brief(&u_full[seg % kPlans], (seg / kPlans) & 1, abort_flag);
+    return warp_wait_working(&u_full[seg % kPlans], (seg / kPlans) & 1, abort_flag, ticks);
   };
   auto release_unit = [&](int seg) {
     __syncwarp();
@@ -731,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
         if (!(ok = acquire())) break;
         store(xv, fv, u % L::kSlots);
         ++u;
+        if (cw == 0 && lane == 0) *ticks = u;
         id1 = id2;
         fk = fk1 * kinv;
         fv = fv1 * vinv;
@@ -824,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       // ---------------------------------------------------------- plan
       for (int seg = 0;; ++seg) {
         if (seg >= kPlans)
-          ok = warp_wait_brief(&u_empty[seg % kPlans], ((seg / kPlans) - 1) & 1, abort_flag);
+          ok = warp_wait_working(&u_empty[seg % kPlans], ((seg / kPlans) - 1) & 1, abort_flag, ticks);
         if (!ok) break;
         Unit& unit = unit_at(seg);
         const bool more = w.pos < w.end;
