@@ -70,6 +70,7 @@ la_status check_kv(const la_cache* c, const void* k, const void* v, la_dtype dty
       !aligned(count, 4))
     return LA_ERR_INVALID_ARG;
   if (dtype != LA_BF16 && dtype != LA_FP16 && dtype != LA_F32) return LA_ERR_INVALID_ARG;
+  if (!cache_grid_fits((int64_t)B * c->Hkv, N, c->page, writes_kv)) return LA_ERR_INVALID_ARG;
   Range r[4];
   cache_ranges(c, r);
   const size_t bytes = (size_t)B * c->Hkv * N * c->d * dtype_bytes(dtype);

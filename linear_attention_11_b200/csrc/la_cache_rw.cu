@@ -323,9 +323,13 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p
   }
 }
 
+constexpr int64_t kMaxGroups = 0x7ffffff0;  // blocks, or warps, of a call's grid
+
+// Pages that N tokens in a row from any place in a page can touch.
+int64_t spans_of(int64_t N, int page) { return 1 + (N - 1 + page - 1) / page; }
+
 template <typename T, int D>
 cudaError_t write_typed(const CacheWriteParams& p, int64_t groups, cudaStream_t stream) {
-  if (groups > 0x7ffffff0) return cudaErrorInvalidValue;
   if (p.N <= kFewTokens) {
     cache_write_kernel<T, D, true><<<dim3((unsigned)((groups + 7) / 8), 2), 256, 0, stream>>>(p);
   } else {
@@ -338,7 +342,6 @@ cudaError_t write_typed(const CacheWriteParams& p, int64_t groups, cudaStream_t 
 template <typename T, int D, int ROWS>
 cudaError_t read_rows(CacheReadParams p, int64_t bh, cudaStream_t stream) {
   const int64_t blocks = (p.N + ROWS - 1) / ROWS, units = blocks * bh;
-  if (units > 0x7ffffff0) return cudaErrorInvalidValue;
   p.blocks = (int)blocks;
   p.bh = (uint32_t)bh;
   cache_read_kernel<T, D, ROWS><<<dim3((unsigned)((units + 7) / 8), 2), 256, 0, stream>>>(p);
@@ -356,17 +359,19 @@ cudaError_t read_typed(CacheReadParams p, int64_t bh, int sms, cudaStream_t stre
 
 }  // namespace
 
+// (a read that takes short runs has few of them)
+bool cache_grid_fits(int64_t bh, int64_t N, int page, bool read) {
+  return (read ? (N + kReadRows - 1) / kReadRows : spans_of(N, page)) <= kMaxGroups / bh;
+}
+
 cudaError_t launch_cache_write(const void* k, const void* v, la_dtype dtype, const la_cache& c,
                                const int32_t* table, const int32_t* start, const int32_t* count,
                                int B, int64_t N, int max_pages, unsigned* status,
                                cudaStream_t stream) {
   CacheWriteParams p{{k, v}, {c.k_codes, c.v_codes}, {c.k_scale, c.v_scale}, table, start, count,
                      status, N, c.num_pages, B, c.Hkv, max_pages, c.page, page_log2(c.page), 0};
-  // N tokens in a row from any place in a page: 1 + ceil((N - 1) / page) pages
-  const int64_t spans = 1 + (N - 1 + c.page - 1) / c.page;
-  if (spans > 0x7fffffff) return cudaErrorInvalidValue;
-  p.spans = (int)spans;
-  const int64_t groups = spans * B * c.Hkv;
+  p.spans = (int)spans_of(N, c.page);
+  const int64_t groups = (int64_t)p.spans * B * c.Hkv;
   if (c.d == 64) {
     if (dtype == LA_BF16) return write_typed<__nv_bfloat16, 64>(p, groups, stream);
     if (dtype == LA_FP16) return write_typed<__half, 64>(p, groups, stream);

@@ -138,6 +138,8 @@ cudaError_t launch_bwd_walk(const la_bf16* q, const la_bf16* k, const la_bf16* v
 // The 8-bit key/value cache (la_cache_* entry points; arguments already checked).
 constexpr int kAttendMaxGroup = 32;    // query heads per kv head
 constexpr int kAttendMaxBatch = 4096;  // sequences of one call
+// Whether a write's or a read's blocks fit a grid (bh = B * Hkv).
+bool cache_grid_fits(int64_t bh, int64_t N, int page, bool read);
 cudaError_t launch_cache_write(const void* k, const void* v, la_dtype dtype, const la_cache& c,
                                const int32_t* table, const int32_t* start, const int32_t* count,
                                int B, int64_t N, int max_pages, unsigned* status,

@@ -147,3 +147,13 @@ def test_binding_refusals(fake):
         with pytest.raises(ValueError, match=match):
             call()
     assert fake.calls == []
+
+
+def test_sizes_beyond_a_grid_are_refused(la):
+    """More pages or runs of tokens than a grid has blocks: an argument error, like other sizes."""
+    N, Hkv = 2 ** 31 - 300, 2
+    for B in (9, 64, 2 ** 20):
+        assert write(la, N=N, B=B, Hkv=Hkv) == 1, B
+    for B in (64, 2 ** 20):
+        there = P((8 << 20) + B * Hkv * N * 64 * 2)   # v behind k
+        assert read(la, N=N, B=B, Hkv=Hkv, v=there) == 1, B
