@@ -355,7 +355,8 @@ typedef struct {
  * The cache holds finite numbers only: an infinity is stored as the largest code
  * of its sign, a NaN as zero, neither counts for the scale, and
  * LA_DEV_NONFINITE is set.
- * Errors: LA_ERR_INVALID_ARG (null, misaligned or overlapping pointers, an
+ * Errors: LA_ERR_INVALID_ARG (null or misaligned pointers, something written that
+ * overlaps something else of the call's, the table and lengths among them, an
  * unknown dtype, sizes <= 0 or such that B * Hkv times the pages that N tokens touch, or when
  * reading times N / 64, pass 2^31 - 16), LA_ERR_UNSUPPORTED (page or d). */
 la_status la_cache_write(const void *k, const void *v, la_dtype dtype, const la_cache *cache,

@@ -64,8 +64,18 @@ bool any_meets(const Range& w, const Range* r, int n) {
   return false;
 }
 
+// The page table and lengths of a call.  Kernels read them again as they go, so nothing that
+// they write may change them.
+void index_ranges(const int32_t* table, const int32_t* len0, const int32_t* len1, int B, int max_pages,
+                  Range (&r)[3]) {
+  r[0] = {table, (size_t)B * max_pages * 4};
+  r[1] = {len0, (size_t)B * 4};
+  r[2] = {len1, (size_t)B * 4};
+}
+
 la_status check_kv(const la_cache* c, const void* k, const void* v, la_dtype dtype,
-                   const int32_t* start, const int32_t* count, int B, int64_t N, bool writes_kv) {
+                   const int32_t* table, const int32_t* start, const int32_t* count, int B,
+                   int64_t N, int max_pages, bool writes_kv) {
   if (!k || !v || !start || !aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) ||
       !aligned(count, 4))
     return LA_ERR_INVALID_ARG;
@@ -76,10 +86,14 @@ la_status check_kv(const la_cache* c, const void* k, const void* v, la_dtype dty
   const size_t bytes = (size_t)B * c->Hkv * N * c->d * dtype_bytes(dtype);
   const Range kr{k, bytes}, vr{v, bytes};
   if (any_meets(kr, r, 4) || any_meets(vr, r, 4)) return LA_ERR_INVALID_ARG;
-  if (writes_kv && meets(kr, vr)) return LA_ERR_INVALID_ARG;
-  if (!writes_kv)
-    for (int i = 0; i < 4; ++i)
-      if (any_meets(r[i], r + i + 1, 3 - i)) return LA_ERR_INVALID_ARG;
+  Range index[3];
+  index_ranges(table, start, count, B, max_pages, index);
+  if (writes_kv) {
+    if (meets(kr, vr) || any_meets(kr, index, 3) || any_meets(vr, index, 3)) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+  }
+  for (int i = 0; i < 4; ++i)
+    if (any_meets(r[i], r + i + 1, 3 - i) || any_meets(r[i], index, 3)) return LA_ERR_INVALID_ARG;
   return LA_OK;
 }
 
@@ -103,7 +117,11 @@ la_status check_attend(const void* q, la_dtype dtype, const la_cache* c, const i
   for (int i = 0; i < 4; ++i) r[i] = cr[i];
   r[4] = {q, rows * c->d * 2};
   r[5] = {lse, rows * 4};
-  if (any_meets({o, rows * c->d * 2}, r, 6) || any_meets(r[5], r, 5)) return LA_ERR_INVALID_ARG;
+  const Range out{o, rows * c->d * 2};
+  if (any_meets(out, r, 6) || any_meets(r[5], r, 5)) return LA_ERR_INVALID_ARG;
+  Range index[3];
+  index_ranges(table, kv_len, q_len, B, max_pages, index);
+  if (any_meets(out, index, 3) || any_meets(r[5], index, 3)) return LA_ERR_INVALID_ARG;
   return LA_OK;
 }
 
@@ -131,7 +149,7 @@ LA_EXPORT la_status la_cache_write(const void* k, const void* v, la_dtype dtype,
                                    const int32_t* start, const int32_t* count, int B, int64_t N,
                                    int max_pages, la_stream stream) {
   la_status st = check_cache(cache, table, B, N, max_pages);
-  if (st == LA_OK) st = check_kv(cache, k, v, dtype, start, count, B, N, false);
+  if (st == LA_OK) st = check_kv(cache, k, v, dtype, table, start, count, B, N, max_pages, false);
   if (st != LA_OK) return st;
   unsigned* status = device_status_ptr();
   if (!status) return LA_ERR_CUDA;
@@ -144,7 +162,7 @@ LA_EXPORT la_status la_cache_read(const la_cache* cache, const int32_t* table,
                                   la_dtype dtype, int B, int64_t N, int max_pages,
                                   la_stream stream) {
   la_status st = check_cache(cache, table, B, N, max_pages);
-  if (st == LA_OK) st = check_kv(cache, k, v, dtype, start, count, B, N, true);
+  if (st == LA_OK) st = check_kv(cache, k, v, dtype, table, start, count, B, N, max_pages, true);
   if (st != LA_OK) return st;
   unsigned* status = device_status_ptr();
   const int sms = device_sms();
@@ -175,9 +193,11 @@ LA_EXPORT la_status la_cache_attend_ws(const void* q, la_dtype dtype, const la_c
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return LA_ERR_WORKSPACE;
   Range r[4];
   cache_ranges(cache, r);
+  Range index[3];
+  index_ranges(table, kv_len, q_len, B, max_pages, index);
   const Range w{workspace, need};
   const size_t rows = (size_t)B * Hq * N;
-  if (any_meets(w, r, 4) || meets(w, {q, rows * cache->d * 2}) ||
+  if (any_meets(w, r, 4) || any_meets(w, index, 3) || meets(w, {q, rows * cache->d * 2}) ||
       meets(w, {o, rows * cache->d * 2}) || meets(w, {lse, rows * 4}))
     return LA_ERR_WORKSPACE;
   return run_attend(q, dtype, cache, table, kv_len, q_len, o, lse, B, Hq, N, max_pages, scale,

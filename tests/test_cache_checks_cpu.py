@@ -157,3 +157,18 @@ def test_sizes_beyond_a_grid_are_refused(la):
     for B in (64, 2 ** 20):
         there = P((8 << 20) + B * Hkv * N * 64 * 2)   # v behind k
         assert read(la, N=N, B=B, Hkv=Hkv, v=there) == 1, B
+
+
+def test_tables_and_lengths_that_the_call_would_write_over(la):
+    """The kernels read them as they go: nothing that a call writes may lie over them."""
+    over_codes, over_scale = P((1 << 20) + 256), P((3 << 20) + 4096)
+    for at in (over_codes, over_scale):
+        for name in ("table", "start", "count"):
+            assert write(la, **{name: at}) == 1, name
+    for name in ("table", "start"):
+        for at in (K, P((9 << 20) + 1024)):
+            assert read(la, **{name: at}) == 1, name
+    for name in ("table", "kv_len", "q_len"):
+        assert attend(la, **{name: P((17 << 20) + 64)}) == 1, name
+        assert attend(la, lse=P(20 << 20), **{name: P((20 << 20) + 4)}) == 1, name
+    assert write(la, table=P((1 << 20) - 12)) == 1   # its last entry
