@@ -377,7 +377,7 @@ def la_decode_steps(S, q, k, v, o=None, stream=None):
 def _cache_fits(cache, table, lengths, tensors):
     kc, vc, ks, vs = cache
     dev, e4m3, f32, i32 = kc.get_device(), torch.float8_e4m3fn, torch.float32, torch.int32
-    pages, B = kc.shape[:2], table.shape[0]
+    pages = kc.shape[:2]
     if not (dev >= 0 and dev == torch.cuda.current_device() and kc.dtype == e4m3
             and vc.dtype == e4m3 and ks.dtype == f32 and vs.dtype == f32 and table.dtype == i32
             and kc.dim() == 4
@@ -387,6 +387,7 @@ def _cache_fits(cache, table, lengths, tensors):
             and vc.get_device() == dev and ks.get_device() == dev and vs.get_device() == dev
             and table.get_device() == dev):
         return False
+    B = table.shape[0]
     for t in lengths:
         if t is not None and not (t.dtype == i32 and t.get_device() == dev and t.dim() == 1
                                   and t.shape[0] == B and t.is_contiguous()):

@@ -172,3 +172,17 @@ def test_tables_and_lengths_that_the_call_would_write_over(la):
         assert attend(la, **{name: P((17 << 20) + 64)}) == 1, name
         assert attend(la, lse=P(20 << 20), **{name: P((20 << 20) + 4)}) == 1, name
     assert write(la, table=P((1 << 20) - 12)) == 1   # its last entry
+
+
+def test_a_table_or_codes_without_dimensions(fake):
+    q, k, cache, table, n = parts()
+    none = torch.zeros((), dtype=torch.int32)
+    with pytest.raises(ValueError, match="max_pages"):
+        api.la_cache_attend(q, cache, none, n)
+    with pytest.raises(ValueError, match="max_pages"):
+        api.la_cache_write(k, k, cache, none, n)
+    with pytest.raises(ValueError, match="num_pages"):
+        api.la_cache_read(cache._replace(k_codes=torch.zeros((), dtype=torch.uint8).view(e4m3)), table, n, k, k.clone())
+    with pytest.raises(ValueError, match="start must be"):
+        api.la_cache_write(k, k, cache, table, none)
+    assert fake.calls == []
