@@ -3,6 +3,9 @@
 Each function takes torch CUDA tensors, passes their device pointers, sizes and
 the current CUDA stream to the C ABI, and raises ``LAError`` on a non-zero
 status.  No arithmetic of the method happens here; there is no CPU fallback.
+With a `stream` the call's work goes there, and an output that the call makes is
+made there; the caller orders that stream after what made the inputs and before
+what reads the results.
 The shared library is loaded on first use and a missing build is an error.
 """
 from __future__ import annotations
@@ -139,6 +142,23 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made(stream, like, shape=None, dtype=None):
+    """A new tensor for what a call on `stream` writes, of `like`'s shape and type unless given: in
+    memory of that stream, which work on the current one may still use otherwise, and kept until
+    the current stream's work at the time it is dropped is done."""
+    def new():
+        return torch.empty_like(like) if shape is None else torch.empty(
+            shape, dtype=dtype or like.dtype, device=like.device)
+    if stream is None:
+        return new()
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = new()
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
 def _on_device(t) -> bool:
     return t.is_cuda
 
@@ -184,7 +204,7 @@ def la_forward(q, k, v, o=None, chunk: int = 64, stream=None):
     """O for q [B,Hq,N,d], k, v [B,Hkv,N,d] (bf16, CUDA); zero initial state."""
     B, Hq, Hkv, N, d = _qkv("la_forward", q, k, v, o)
     if o is None:
-        o = torch.empty_like(q)
+        o = _made(stream, q)
     _check("la_forward", load_library().la_forward(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), B, Hq, Hkv, N, d, chunk, _stream(stream)))
     return o
@@ -195,7 +215,7 @@ def la_forward_state(q, k, v, S=None, o=None, chunk: int = 64, stream=None):
     B, Hq, Hkv, N, d = _qkv("la_forward_state", q, k, v, o)
     _state("la_forward_state", "S", S, B, Hkv, d)
     if o is None:
-        o = torch.empty_like(q)
+        o = _made(stream, q)
     _check("la_forward_state", load_library().la_forward_state(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(S), B, Hq, Hkv, N, d, chunk, _stream(stream)))
     return o
@@ -222,7 +242,7 @@ def la_forward_noalloc(q, k, v, S=None, o=None, chunk: int = 64, stream=None):
     B, Hq, Hkv, N, d = _qkv("la_forward_noalloc", q, k, v, o)
     _state("la_forward_noalloc", "S", S, B, Hkv, d)
     if o is None:
-        o = torch.empty_like(q)
+        o = _made(stream, q)
     _check("la_forward_noalloc", load_library().la_forward_noalloc(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(S), B, Hq, Hkv, N, d, chunk, _stream(stream)))
     return o
@@ -292,7 +312,7 @@ def la_segment_state(k, v, S=None, chunk: int = 64, stream=None):
     B, _, Hkv, N, d = _qkv("la_segment_state", k, k, v)
     _state("la_segment_state", "S", S, B, Hkv, d)
     if S is None:
-        S = torch.empty(B, Hkv, d, d, dtype=torch.float32, device=k.device)
+        S = _made(stream, k, (B, Hkv, d, d), torch.float32)
     _check("la_segment_state", load_library().la_segment_state(
         _ptr(k), _ptr(v), _ptr(S), B, Hkv, N, d, chunk, _stream(stream)))
     return S
@@ -308,7 +328,7 @@ def la_state_prefix(states, seg: int, S0=None, S=None, stream=None):
     _state("la_state_prefix", "S0", S0, B, Hkv, d)
     _state("la_state_prefix", "S", S, B, Hkv, d)
     if S is None:
-        S = torch.empty(B, Hkv, d, d, dtype=torch.float32, device=states.device)
+        S = _made(stream, states, (B, Hkv, d, d))
     _check("la_state_prefix", load_library().la_state_prefix(
         _ptr(states), _ptr(S0), _ptr(S), nseg, seg, B, Hkv, d, _stream(stream)))
     return S
@@ -321,8 +341,8 @@ def la_backward(q, k, v, dO, S0=None, dSf=None, want_dS0: bool = False, chunk: i
     B, Hq, Hkv, N, d = _qkv("la_backward", q, k, v, dO)
     _state("la_backward", "S0", S0, B, Hkv, d)
     _state("la_backward", "dSf", dSf, B, Hkv, d)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dS0 = torch.empty(B, Hkv, d, d, dtype=torch.float32, device=q.device) if want_dS0 else None
+    dq, dk, dv = (_made(stream, t) for t in (q, k, v))
+    dS0 = _made(stream, q, (B, Hkv, d, d), torch.float32) if want_dS0 else None
     _check("la_backward", load_library().la_backward(
         _ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(S0), _ptr(dSf), _ptr(dq), _ptr(dk), _ptr(dv),
         _ptr(dS0), B, Hq, Hkv, N, d, chunk, _stream(stream)))
@@ -333,7 +353,7 @@ def la_forward_f32(q, k, v, o=None, S=None, chunk: int = 64, stream=None):
     B, Hq, Hkv, N, d = _qkv("la_forward_f32", q, k, v, o, dtype=torch.float32)
     _state("la_forward_f32", "S", S, B, Hkv, d)
     if o is None:
-        o = torch.empty_like(q)
+        o = _made(stream, q)
     _check("la_forward_f32", load_library().la_forward_f32(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(S), B, Hq, Hkv, N, d, chunk, _stream(stream)))
     return o
@@ -352,7 +372,7 @@ def la_decode_step(S, q, k, v, o=None, stream=None):
     if S is None:
         raise ValueError("la_decode_step: S is required")
     if o is None:
-        o = torch.empty_like(q)
+        o = _made(stream, q)
     _check("la_decode_step", load_library().la_decode_step(
         _ptr(S), _ptr(q), _ptr(k), _ptr(v), _ptr(o), B, Hq, k.shape[1], d, _stream(stream)))
     return o
@@ -365,7 +385,7 @@ def la_decode_steps(S, q, k, v, o=None, stream=None):
     if S is None:
         raise ValueError("la_decode_steps: S is required")
     if o is None:
-        o = torch.empty_like(q)
+        o = _made(stream, q)
     _check("la_decode_steps", load_library().la_decode_steps(
         _ptr(S), _ptr(q), _ptr(k), _ptr(v), _ptr(o), B, Hq, k.shape[1], d, steps, _stream(stream)))
     return o
@@ -504,7 +524,7 @@ def la_cache_attend(q, cache: la_cache, table, kv_len, q_len=None, o=None, lse=N
         raise ValueError(f"{fn}: kv_len is required")
     B, Hq, N, d = shape
     if o is None:
-        o = torch.empty_like(q)
+        o = _made(stream, q)
     args = (q.data_ptr(), DTYPES[dtype], c, table.data_ptr(), kv_len.data_ptr(), _address(q_len),
             o.data_ptr(), _address(lse), B, Hq, N, table.shape[1],
             1.0 / math.sqrt(d) if scale is None else scale)

@@ -26,3 +26,44 @@ def test_a_workspace_over_the_table_or_a_length(la):
         assert e.value.code == 5
     got = la.la_cache_attend(q, dev, t.clone(), ints([700], DEV), workspace=room[:need])
     assert torch.equal(got, ref) and la.la_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("call", ["cache_attend", "forward", "forward_state", "decode_step", "decode_steps",
+                                  "backward", "segment_state"])
+def test_what_a_call_makes_is_its_streams(la, call):
+    """An output that a call on another stream makes does not lie in memory that the current stream has
+    just given back and may still be working on."""
+    B, H, N, d = 2, 4, 1024, 128
+    q, k, v = (normal(i, B, H, N, d).bfloat16().to(DEV) for i in range(3))
+    S = torch.zeros(B, H, d, d, device=DEV)
+    s = torch.cuda.Stream()
+    if call == "cache_attend":
+        cache, table = filled_cache([1100, 1030], H, 32, d, 1)
+        dev, t, n = to_device(la, cache, DEV), torch.from_numpy(table).to(DEV), ints([1100, 1030], DEV)
+        run = lambda stream: la.la_cache_attend(q, dev, t, n, stream=stream)  # noqa: E731
+    elif call == "decode_step":
+        one = [x[:, :, 0].contiguous() for x in (q, k, v)]
+        run = lambda stream: la.la_decode_step(S.clone(), *one, stream=stream)  # noqa: E731
+    elif call == "decode_steps":
+        some = [x[:, :, :8].contiguous() for x in (q, k, v)]
+        run = lambda stream: la.la_decode_steps(S.clone(), *some, stream=stream)  # noqa: E731
+    elif call == "backward":
+        run = lambda stream: la.la_backward(q, k, v, q, stream=stream)[0]  # noqa: E731
+    elif call == "segment_state":
+        run = lambda stream: la.la_segment_state(k, v, stream=stream)  # noqa: E731
+    else:
+        run = lambda stream: getattr(la, "la_" + call)(q, k, v, stream=stream)  # noqa: E731
+    ref = run(None)
+    torch.cuda.synchronize()
+    freed = {ref.data_ptr()}
+    keep, ref = ref.clone(), None
+    for _ in range(4):                 # memory of this size that the current stream gave back
+        x = torch.empty_like(keep)
+        freed.add(x.data_ptr())
+        del x
+    torch.cuda.synchronize()
+    o = run(s)
+    torch.cuda.synchronize()
+    assert torch.equal(o, keep)
+    assert o.data_ptr() not in freed
+    assert la.la_device_status() == (0, 0)
