@@ -383,7 +383,8 @@ la_status la_cache_read(const la_cache *cache, const int32_t *table, const int32
  * of o and lse are left as they were.
  *   q, o      bf16 or fp16 [B,Hq,N,d], o not overlapping q or the cache
  *   lse       fp32 [B,Hq,N], or null
- *   scale     finite; usually 1/sqrt(d)
+ *   scale     finite; usually 1/sqrt(d).  Scores, and scale times a row's largest |q| and a
+ *             page's scale, are within fp32's range
  * Scores, the softmax's sums and the products' sums are held in fp32.  Weights enter the
  * product with the values as fp16, 2^-11 of each or, of the small ones, 2^-32 of the row's
  * largest.  Scales go with them or with the codes:

@@ -214,6 +214,15 @@ constexpr float kAttendShift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Whether a row's reference maximum m (log2 units) is so large that 2^(score f - m) needs the
+// product rounded as m was: exact, it is up to half a place of m away from m, and past 2^27 that
+// overflowed weights, or left none (finite inputs gave NaN, and zeros).  There the maximum is
+// followed without slack, too.  (True of -infinity as well: a row without weights is at no loss.)
+__device__ __forceinline__ bool far_off(float m) { return fabsf(m) > 4194304.f; }
+
+// How far above m a score may lie that leaves m as it is.
+__device__ __forceinline__ float slack_of(float m) { return far_off(m) ? 0.f : 8.f; }
+
 // n / m for n >= 0, m > 0; in 32 bits where n has them (a 64-bit division takes a
 // few hundred cycles).
 __device__ __forceinline__ int64_t div_short(int64_t n, int64_t m) {

@@ -43,7 +43,6 @@ constexpr int kThreads = 640, kConvert = 256;
 constexpr int kIssue = 16, kPlan = 17;  // the warps that issue products and plan
 constexpr int kPlans = 4;               // units that the plan is ahead at most
 constexpr float kShift = kAttendShift;
-constexpr float kSlack = 8.f;  // growth of a row's maximum that is let pass
 // Key tiles whose products O takes up in tensor memory; then it is added to its part in
 // the workspace and begins again.  The products cut off what lies below the sum's last
 // places and do not round it: over 2^18 tokens in one sum, all values 1, o was 0.9937.
@@ -178,6 +177,16 @@ __device__ __forceinline__ int load_word(const int* p, bool there, int other) {
       : "=&r"(v)
       : "l"(p), "r"((uint32_t)there), "r"(other));
   return v;
+}
+
+// By a whole warp: 16 columns of its lanes of tensor memory by each lane's factor.
+__device__ __forceinline__ void times(uint32_t at, float a) {
+  uint32_t y[16];
+  tmem_ld16(at, y);
+  tmem_wait_ld();
+#pragma unroll
+  for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a);
+  tmem_st16(at, y);
 }
 
 // a z + x, four fp32 numbers of x as they come from tensor memory.
@@ -494,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
           }
           top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]);
           const float mt = top[0] == -INFINITY ? -INFINITY : top[0] * f;
-          const bool grows = mt > m + kSlack || (m == -INFINITY && mt > -INFINITY);
-          if (__any_sync(0xffffffffu, grows)) {
+          const bool grows = mt - m > slack_of(m);  // (false for two infinities)
+          if (__any_sync(0xffffffffu, grows || far_off(m))) {
             // a new reference: the sum so far and O go by 2^(old - new)
             const float a = grows ? exp2_fast(m - mt) : 1.f;
             if (grows) m = mt;
@@ -503,18 +512,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
             lost *= a;
             if (i > i0) {  // the product of the tile before is in: it was issued before these scores
 #pragma unroll 1
-              for (int k = 0; k < D / 16; ++k) {
-                uint32_t y[16];
-                tmem_ld16(ot + k * 16, y);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a);
-                tmem_st16(ot + k * 16, y);
-              }
+              for (int k = 0; k < D / 16; ++k) times(ot + k * 16, a);
+            }
+            // scores of rows far off are multiplied where they lie: rarely, and in little code
+            if (__any_sync(0xffffffffu, far_off(m))) {
+#pragma unroll 1
+              for (int k = 0; k < kKeys / 16; ++k) times(st + k * 16, far_off(m) ? f : 1.f);
+              tmem_wait_st();
             }
           }
           const float off = kShift - (m == -INFINITY ? 0.f : m);
-          const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+          const float f1 = far_off(m) ? 1.f : f;
+          const float2 f2 = make_float2(f1, f1), off2 = make_float2(off, off);
           float2 sum = make_float2(0.f, 0.f), sum2 = sum;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {

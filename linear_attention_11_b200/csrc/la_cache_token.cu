@@ -50,7 +50,6 @@ constexpr int kTile = 64;        // tokens of a stage
 constexpr int kConsumers = 128;  // four warps
 constexpr int kThreads = kConsumers + 32;
 constexpr float kShift = kAttendShift;
-constexpr float kSlack = 8.f;   // growth of a row's maximum that is let pass
 // Tokens whose products a warp's sums in registers take up; then they are added to those in
 // its buffer and begin again.  The products cut off what lies below the sum's last places and
 // do not round it: over 2^18 tokens, all values 1, o was 0.998 to 0.999.  (256 sequences 198.3
@@ -632,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
             if (!FEW) top = max3(top, score(u, k, 2 % SC), score(u, k, 3 % SC));
             mx[k] = u ? fmaxf(mx[k], top * f[u][k]) : top * f[u][k];
           }
-          grows |= mx[k] > m[k] + kSlack || (m[k] == -INFINITY && mx[k] > -INFINITY);
+          grows |= mx[k] - m[k] > slack_of(m[k]);  // (not for two infinities)
         }
         if (__any_sync(0xffffffffu, grows)) {
           float a[2];
@@ -656,6 +655,14 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float off = kShift - (m[k] == -INFINITY ? 0.f : m[k]);
+          if (far_off(m[k])) {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+              for (int j = 0; j < SC; ++j) score(u, k, j) *= f[u][k];
+              f[u][k] = 1.f;
+            }
+          }
           float sum = 0.f;
 #pragma unroll
           for (int u = 0; u < SUB; ++u) {
