@@ -400,8 +400,9 @@ la_status la_cache_read(const la_cache *cache, const int32_t *table, const int32
  * (la_cache_attend_ws: 256-byte aligned, at least
  * la_cache_attend_workspace_bytes(), not in use by anything else until the
  * call's work has finished: captured graphs that may run at the same time need
- * one each).  The size is 0 for sizes that the calls refuse.  The same inputs give
- * the same bits.
+ * one each).  The size is 0 for sizes that the calls refuse.  The same call gives the
+ * same bits; the last bits of a sequence's rows may differ between batches and between widths
+ * of the table, which decide where it is split.
  * Errors as la_cache_write; LA_ERR_UNSUPPORTED also for Hq / Hkv > 32, B > 4096
  * and fp32; LA_ERR_WORKSPACE. */
 size_t la_cache_attend_workspace_bytes(int B, int Hq, int Hkv, int64_t N, int d);

@@ -229,8 +229,9 @@ __device__ __forceinline__ int64_t div_short(int64_t n, int64_t m) {
   return (n | m) >> 32 ? n / m : (int64_t)((uint32_t)n / (uint32_t)m);
 }
 
-// The line in equal shares for at most `blocks` blocks, of four tiles or more: block k
-// has [begin(k), begin(k + 1)).
+// The line in equal shares for at most `blocks` blocks, of about four places where it is
+// short (two at least; those of a unit's cost are no tiles, so a block may have none): block k has
+// [begin(k), begin(k + 1)).
 struct Shares {
   int64_t each;
   int n, more;  // shares; how many of them have one more

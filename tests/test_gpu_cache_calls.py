@@ -1,8 +1,11 @@
 """Calls of the 8-bit cache's entry points that a program could make by mistake, or from two streams."""
+import numpy as np
 import pytest
 import torch
 
-from _cache_cases import filled_cache, ints, normal, to_device
+from oracle import cache as oc
+
+from _cache_cases import attend_bounds, filled_cache, ints, normal, to_device
 
 pytestmark = pytest.mark.gpu
 
@@ -66,4 +69,29 @@ def test_what_a_call_makes_is_its_streams(la, call):
     torch.cuda.synchronize()
     assert torch.equal(o, keep)
     assert o.data_ptr() not in freed
+    assert la.la_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("G,N,d", [(4, 64, 128), (1, 1, 64), (4, 5, 128), (2, 300, 64)])
+def test_sequences_on_the_same_pages(la, G, N, d):
+    """Over a short table units are whole: two sequences on one prompt's pages, the same call in another
+    batch and repeated calls give the same bits.  Over a long one they are cut by the whole batch's line:
+    the same to what the order of fp32 sums and the reference maxima (weights are rounded relative to them)
+    leave open, once for each of the two."""
+    cache, table = filled_cache([500], 2, 32, d, 12)
+    dev = to_device(la, cache, DEV)
+    q = normal(2, 1, 2 * G, N, d).bfloat16().expand(2, -1, -1, -1).contiguous()
+    short = torch.from_numpy(table).to(DEV).expand(2, -1).contiguous()
+    wide = torch.full((2, 4096), -1, dtype=torch.int32, device=DEV)
+    wide[:, :short.shape[1]] = short
+    n = ints([500, 500], DEV)
+    o = la.la_cache_attend(q.to(DEV), dev, short, n)
+    assert torch.equal(o[0], o[1])
+    assert torch.equal(la.la_cache_attend(q[:1].to(DEV), dev, short[:1], n[:1]), o[:1])
+    ref = oc.attend(cache, table, q[:1].double().numpy(), [500], [N], d ** -0.5)
+    cut = la.la_cache_attend(q.to(DEV), dev, wide, n)
+    assert torch.equal(la.la_cache_attend(q.to(DEV), dev, wide, n), cut)
+    bound = 2 * attend_bounds(ref, 500, d, q.dtype)[0][0]
+    for x in (cut[0], cut[1]):
+        assert (np.abs((x - o[0]).double().cpu().numpy()) <= bound).all()
     assert la.la_device_status() == (0, 0)
