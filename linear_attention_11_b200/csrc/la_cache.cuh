@@ -209,6 +209,13 @@ __device__ __forceinline__ void add_up(float& l, float& lost, float x) {
   l = sum;
 }
 
+// The larger one, or the NaN: of a page's scale, where it shows that the page was never written.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Weights are held as 2^kAttendShift at a row's reference maximum.
 constexpr float kAttendShift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;

@@ -693,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttendParams 
       // a second one rounds once)
       auto store = [&](const uint4 (&x)[kLoads], float factor, int slot) {
         const uint32_t dst = base + L::kSlotOff + slot * L::kSlot + store_at;
-        const uint32_t fw = pack2<__half>(fmaxf(factor, 0x1p-14f), fminf(factor * 0x1p14f, 1.f));
+        const bool two = factor < 0x1p-14f;  // (a NaN stays in the first)
+        const uint32_t fw = pack2<__half>(two ? 0x1p-14f : factor, two ? factor * 0x1p14f : 1.f);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
           const uint32_t fj = __shfl_sync(0xffffffffu, fw, (j * kRowsPerLoad + sub) >> 4);

@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
 #pragma unroll
           for (int u = 0; u < SUB; ++u) {
             // (not zero: a masked score stays at -infinity)
-            f[u][k] = fmaxf(rf[k] * sc[u].x, 1.17549435e-38f);
+            f[u][k] = max_or_nan(rf[k] * sc[u].x, 1.17549435e-38f);
             float top = fmaxf(score(u, k, 0), score(u, k, 1));
             if (!FEW) top = max3(top, score(u, k, 2 % SC), score(u, k, 3 % SC));
             mx[k] = u ? fmaxf(mx[k], top * f[u][k]) : top * f[u][k];

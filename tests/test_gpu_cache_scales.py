@@ -73,3 +73,20 @@ def test_small_keys_before_large_ones(la, d, G, page, log_r):
     # scales differ by 2^4 among pages of a kind
     check(la, cache, table, q, [n, 40], [n, 40], d ** -0.5 * 2.0 ** -log_r,
           2.0 ** -32 * largest if log_r < -18 else 0, 0)
+
+
+@pytest.mark.parametrize("N", [1, 12, 40])
+@pytest.mark.parametrize("name", ["k_scale", "v_scale", "k", "v"])
+def test_a_page_that_was_never_written_shows(la, N, name):
+    """NaN in a page's scale, or in a code: the rows that see it are NaN, not something finite."""
+    cache, table = filled_cache([70, 70], 1, 16, 64, 4)
+    bad = cache[name]
+    if name in "kv":
+        bad[table[0, 1], 0, 3, 5] = 0x7F
+    else:
+        bad[table[0, 1], 0] = np.nan
+    q = normal(2, 2, 2, N, 64).half().to(DEV)
+    o = la.la_cache_attend(q, to_device(la, cache, DEV), torch.from_numpy(table).to(DEV), ints([70, 70], DEV))
+    seen = o[0].isnan().any(-1)
+    assert seen.all() and torch.isfinite(o[1]).all()
+    la.la_device_status()
